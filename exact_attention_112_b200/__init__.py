@@ -30,6 +30,9 @@ __all__ = [
     "fa_status_string", "fa_device_status", "fa_debug_wait_timeout", "fa_launch_count",
     "fa_profile_enable", "fa_profile_read",
     "attention_forward", "attention_backward",
+    "Rope", "PagedKV", "rope_inv_freq", "fa_rope", "fa_rope_bwd", "rope_forward", "rope_backward",
+    "rope_attention_forward", "rope_attention_backward", "fa_paged_append", "fa_paged_fwd",
+    "fa_paged_fwd_workspace_bytes", "paged_attention", "paged_step",
 ]
 
 (FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_DEVICE_TIMEOUT,
@@ -110,6 +113,8 @@ def lib() -> ctypes.CDLL:
             L.fa_launch_count.restype = ctypes.c_ulonglong
             L.fa_debug_wait_timeout.argtypes = [ctypes.c_uint, vp]
             L.fa_debug_wait_timeout.restype = i
+            from . import paged
+            paged._declare(L)
             _lib = L
     return _lib
 
@@ -519,3 +524,8 @@ def attention_backward(q, k, v, o, lse, dO, causal=False, scale=None, key_bias=N
     fa_bwd(q, k, v, o, lse, dO, dq, dk, dv, ws, causal=causal, scale=scale,
            key_bias=key_bias, stream=stream)
     return dq, dk, dv
+
+
+from .paged import (  # noqa: E402
+    PagedKV, Rope, fa_paged_append, fa_paged_fwd, fa_paged_fwd_workspace_bytes, fa_rope, fa_rope_bwd, paged_attention,
+    paged_step, rope_attention_backward, rope_attention_forward, rope_backward, rope_forward, rope_inv_freq)

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "fa.h"
+#include "fa_host.h"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -126,6 +127,16 @@ thread_local bool t_prof_on = false;
 thread_local std::vector<ProfRecord> t_prof;
 
 }  // namespace
+
+int fa::host_device(int **err, int *sm_count) {
+    int dev;
+    const int st = current_device(&dev);
+    return st != FA_OK ? st : device_setup(dev, err, sm_count);
+}
+
+int fa::host_encoder(PFN_cuTensorMapEncodeTiled_v12000 *fn) { return get_encoder(fn); }
+
+unsigned long long fa::host_wait_limit_ns() { return kDefaultTimeoutNs; }
 
 void fa::note_launch(unsigned n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 

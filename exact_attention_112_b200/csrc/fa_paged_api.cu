@@ -1,0 +1,235 @@
+// fa_paged_api.cu -- the C ABI of the rotary-position and paged-cache operators
+// (declared in include/fa.h): argument validation and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "fa.h"
+#include "fa_host.h"
+#include "fa_internal.h"
+#include "fa_paged_internal.h"
+
+namespace {
+
+bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+int check_rope(const fa_rope_spec *r, int D) {
+    if (!r || !r->inv_freq || !aligned(r->inv_freq, 8)) return FA_ERR_INVALID_ARG;
+    if (r->rot_dim < 16 || r->rot_dim % 16 != 0 || r->rot_dim > D) return FA_ERR_INVALID_ARG;
+    if (r->interleaved != 0 && r->interleaved != 1) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(r->scale) || !(r->scale > 0.f)) return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+// Strides of a tensor with extents n[] (outermost first) and D contiguous
+// values: given or contiguous; extents of 1 need none.  `low` is the least
+// stride allowed.
+template <int K>
+int get_strides(const long long *given, const long long (&n)[K], int D, long long low, long long (&s)[K]) {
+    long long run = D;
+    for (int i = K - 1; i >= 0; --i) {
+        s[i] = given ? given[i] : run;
+        run *= n[i];
+        if (n[i] <= 1) {
+            s[i] = D;
+            continue;
+        }
+        if (s[i] % 8 != 0 || s[i] < low || s[i] > (1LL << 38)) return FA_ERR_INVALID_ARG;
+    }
+    return FA_OK;
+}
+
+int rope_impl(const void *q, const long long *qs, void *qo, const long long *qos, int Hq, const void *k,
+              const long long *ks, void *ko, const long long *kos, int Hk, int B, int N, int D,
+              const fa_rope_spec *rope, const int *positions, long long pos_stride, int pos0, int dtype, void *stream,
+              float sign) {
+    if (B < 1 || Hq < 1 || Hk < 0 || N < 0 || pos_stride < 0) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
+    if (D < 16 || D > 512 || D % 8 != 0) return FA_ERR_UNSUPPORTED;
+    int st = check_rope(rope, D);
+    if (st != FA_OK) return st;
+    const long long rows = static_cast<long long>(B) * N;
+    if (rows > INT32_MAX || rows * ((D + 15) / 16) > INT32_MAX || Hq > 65536 || Hk > 65536) return FA_ERR_INVALID_ARG;
+    if (!positions && static_cast<long long>(pos0) + N > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if (N == 0) return FA_OK;
+    if (!q || !qo || (Hk > 0 && (!k || !ko)) || (Hk == 0 && (k || ko))) return FA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(qo, 16) || !aligned(k, 16) || !aligned(ko, 16) || !aligned(positions, 4))
+        return FA_ERR_INVALID_ARG;
+    fa::RopeParams p{};
+    long long s[3];
+    auto fill = [&](fa::RopeTensor &t, const void *in, const long long *is, void *out, const long long *os, int H) {
+        const long long n[3] = {B, H, N};
+        int e = get_strides(is, n, D, 0, s);
+        if (e != FA_OK) return e;
+        t.in = in;
+        t.out = out;
+        t.H = H;
+        t.in_b = s[0]; t.in_h = s[1]; t.in_n = s[2];
+        if ((e = get_strides(os, n, D, D, s)) != FA_OK) return e;
+        t.out_b = s[0]; t.out_h = s[1]; t.out_n = s[2];
+        return static_cast<int>(FA_OK);
+    };
+    if ((st = fill(p.q, q, qs, qo, qos, Hq)) != FA_OK) return st;
+    if (Hk > 0 && (st = fill(p.k, k, ks, ko, kos, Hk)) != FA_OK) return st;
+    p.B = B;
+    p.N = N;
+    p.D = D;
+    p.rot = rope->rot_dim;
+    p.interleaved = rope->interleaved;
+    p.scale = rope->scale;
+    p.sign = sign;
+    p.inv_freq = rope->inv_freq;
+    p.positions = positions;
+    p.pos_stride = pos_stride;
+    p.pos0 = pos0;
+    int *err = nullptr, sms = 1;
+    if ((st = fa::host_device(&err, &sms)) != FA_OK) return st;
+    return fa::launch_rope(p, dtype == FA_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                                       : FA_ERR_CUDA;
+}
+
+int check_cache(const fa_paged_kv *kv, fa::PagedCache *c) {
+    if (!kv) return FA_ERR_INVALID_ARG;
+    if (kv->dtype != FA_F16 && kv->dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
+    if (kv->D != 64 && kv->D != 128) return FA_ERR_UNSUPPORTED;
+    if (kv->num_seqs < 1 || kv->max_pages < 1 || kv->num_pages < 1 || kv->num_kv_heads < 1) return FA_ERR_INVALID_ARG;
+    if (kv->page_size < 8 || kv->page_size % 8 != 0 || kv->page_size > 65536) return FA_ERR_INVALID_ARG;
+    if (static_cast<long long>(kv->max_pages) * kv->page_size > (1 << 30)) return FA_ERR_INVALID_ARG;
+    if (kv->num_seqs > (1 << 24) || kv->num_kv_heads > 65536) return FA_ERR_INVALID_ARG;
+    if (!kv->k_cache || !kv->v_cache || !kv->seq_lens || !kv->page_table) return FA_ERR_INVALID_ARG;
+    if (!aligned(kv->k_cache, 16) || !aligned(kv->v_cache, 16) || !aligned(kv->page_table, 4) ||
+        !aligned(kv->seq_lens, 4))
+        return FA_ERR_INVALID_ARG;
+    if (kv->num_seqs > 1 && kv->table_stride < kv->max_pages) return FA_ERR_INVALID_ARG;
+    const long long n[3] = {kv->num_pages, kv->num_kv_heads, kv->page_size};
+    long long s[3];
+    int st;
+    if ((st = get_strides(kv->k_strides, n, kv->D, kv->D, s)) != FA_OK) return st;
+    c->k_page = s[0]; c->k_head = s[1]; c->k_tok = s[2];
+    if ((st = get_strides(kv->v_strides, n, kv->D, kv->D, s)) != FA_OK) return st;
+    c->v_page = s[0]; c->v_head = s[1]; c->v_tok = s[2];
+    c->k = kv->k_cache;
+    c->v = kv->v_cache;
+    c->table = kv->page_table;
+    c->table_stride = kv->table_stride;
+    c->seq_lens = kv->seq_lens;
+    c->num_seqs = kv->num_seqs;
+    c->max_pages = kv->max_pages;
+    c->num_pages = kv->num_pages;
+    c->page_size = kv->page_size;
+    c->Hkv = kv->num_kv_heads;
+    c->D = kv->D;
+    return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_rope(const void *q, const long long *q_strides, void *q_out, const long long *q_out_strides, int Hq,
+            const void *k, const long long *k_strides, void *k_out, const long long *k_out_strides, int Hk, int B,
+            int N, int D, const fa_rope_spec *rope, const int *positions, long long pos_stride, int pos0, int dtype,
+            void *stream) {
+    return rope_impl(q, q_strides, q_out, q_out_strides, Hq, k, k_strides, k_out, k_out_strides, Hk, B, N, D, rope,
+                     positions, pos_stride, pos0, dtype, stream, 1.f);
+}
+
+int fa_rope_bwd(const void *dq_out, const long long *dq_out_strides, void *dq, const long long *dq_strides, int Hq,
+                const void *dk_out, const long long *dk_out_strides, void *dk, const long long *dk_strides, int Hk,
+                int B, int N, int D, const fa_rope_spec *rope, const int *positions, long long pos_stride, int pos0,
+                int dtype, void *stream) {
+    return rope_impl(dq_out, dq_out_strides, dq, dq_strides, Hq, dk_out, dk_out_strides, dk, dk_strides, Hk, B, N, D,
+                     rope, positions, pos_stride, pos0, dtype, stream, -1.f);
+}
+
+int fa_paged_append(const fa_paged_kv *kv, const void *k, const long long *k_strides, const void *v,
+                    const long long *v_strides, const int *cu_seqlens_q, int total_q, const fa_rope_spec *rope,
+                    const int *positions, const void *q, const long long *q_strides, void *q_out,
+                    const long long *q_out_strides, int Hq, void *stream) {
+    fa::AppendParams p{};
+    int st = check_cache(kv, &p.kv);
+    if (st != FA_OK) return st;
+    if (total_q < 0 || total_q > (1 << 28) || Hq < 0 || Hq > 65536) return FA_ERR_INVALID_ARG;
+    if (rope && (st = check_rope(rope, kv->D)) != FA_OK) return st;
+    if (Hq == 0 ? (q || q_out) : !rope) return FA_ERR_INVALID_ARG;
+    if (!cu_seqlens_q || !aligned(cu_seqlens_q, 4) || !aligned(positions, 4)) return FA_ERR_INVALID_ARG;
+    if (total_q == 0) return FA_OK;
+    if (!k || !v || (Hq > 0 && (!q || !q_out))) return FA_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16)) return FA_ERR_INVALID_ARG;
+    const long long nk[2] = {kv->num_kv_heads, total_q}, nq[2] = {Hq, total_q};
+    long long s[2];
+    if ((st = get_strides(k_strides, nk, kv->D, 0, s)) != FA_OK) return st;
+    p.k_h = s[0]; p.k_n = s[1];
+    if ((st = get_strides(v_strides, nk, kv->D, 0, s)) != FA_OK) return st;
+    p.v_h = s[0]; p.v_n = s[1];
+    if ((st = get_strides(q_strides, nq, kv->D, 0, s)) != FA_OK) return st;
+    p.q_h = s[0]; p.q_n = s[1];
+    if ((st = get_strides(q_out_strides, nq, kv->D, kv->D, s)) != FA_OK) return st;
+    p.qo_h = s[0]; p.qo_n = s[1];
+    p.k = k;
+    p.v = v;
+    p.q = q;
+    p.q_out = q_out;
+    p.H = Hq;
+    p.T = total_q;
+    p.cu = cu_seqlens_q;
+    if (rope) {
+        p.rot = rope->rot_dim;
+        p.interleaved = rope->interleaved;
+        p.scale = rope->scale;
+        p.inv_freq = rope->inv_freq;
+        p.positions = positions;
+    }
+    int *err = nullptr, sms = 1;
+    if ((st = fa::host_device(&err, &sms)) != FA_OK) return st;
+    return fa::launch_paged_append(p, kv->dtype == FA_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_paged_fwd_workspace_bytes(const fa_paged_kv *kv, int Hq, int max_seqlen_q) {
+    fa::PagedCache c;
+    if (check_cache(kv, &c) != FA_OK || Hq < 1 || Hq % c.Hkv != 0 || Hq / c.Hkv > 128 || max_seqlen_q < 0) return 0;
+    return 256;
+}
+
+int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_strides, void *o,
+                 const long long *o_strides, float *lse, const int *cu_seqlens_q, int total_q, int max_seqlen_q,
+                 int Hq, int causal, float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    fa::PagedFwdParams p{};
+    int st = check_cache(kv, &p.kv);
+    if (st != FA_OK) return st;
+    if (Hq < 1 || Hq % kv->num_kv_heads != 0 || Hq / kv->num_kv_heads > 128) return FA_ERR_INVALID_ARG;
+    if (total_q < 0 || max_seqlen_q < 0 || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
+    if (static_cast<long long>(Hq) * total_q > INT32_MAX || total_q > (1 << 28)) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+    if (!cu_seqlens_q || !aligned(cu_seqlens_q, 4)) return FA_ERR_INVALID_ARG;
+    if (total_q == 0 || max_seqlen_q == 0) return FA_OK;
+    if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 16)) return FA_ERR_INVALID_ARG;
+    const long long n[2] = {Hq, total_q};
+    long long s[2];
+    if ((st = get_strides(q_strides, n, kv->D, kv->D, s)) != FA_OK) return st;
+    p.q_h = s[0]; p.q_n = s[1];
+    if ((st = get_strides(o_strides, n, kv->D, kv->D, s)) != FA_OK) return st;
+    p.o_h = s[0]; p.o_n = s[1];
+    if (!workspace || workspace_bytes < fa_paged_fwd_workspace_bytes(kv, Hq, max_seqlen_q)) return FA_ERR_WORKSPACE;
+    p.q = q;
+    p.o = o;
+    p.lse = lse;
+    p.cu = cu_seqlens_q;
+    p.T = total_q;
+    p.max_q = max_seqlen_q < total_q ? max_seqlen_q : total_q;
+    p.H = Hq;
+    p.G = Hq / kv->num_kv_heads;
+    p.causal = causal;
+    p.qk_scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    int sms = 1;
+    if ((st = fa::host_device(&p.err, &sms)) != FA_OK) return st;
+    p.timeout_ns = fa::host_wait_limit_ns();
+    return fa::launch_paged_fwd(p, kv->dtype == FA_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,102 @@
+// fa_paged_internal.h -- structures shared between the C-ABI layer and the
+// kernels of the rotary-position and paged-cache operators.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace fa {
+
+// ---------------------------------------------------------------- rotation
+// One 16-bit tensor [B, H, N, D] seen through its strides (elements), D
+// contiguous.  H == 0: absent.
+struct RopeTensor {
+    const void *in;
+    void *out;
+    long long in_b, in_h, in_n;
+    long long out_b, out_h, out_n;
+    int H;
+};
+
+struct RopeParams {
+    RopeTensor q, k;
+    int B, N, D;
+    int rot;                   // rotated values per row, a multiple of 16
+    int interleaved;           // pairs (2i, 2i+1) instead of (i, i + rot/2)
+    float scale;               // multiplies cos and sin
+    float sign;                // +1 forward, -1 transpose (backward)
+    const double *inv_freq;    // [rot / 2] radians per position
+    const int *positions;      // [B or 1, N] or nullptr
+    long long pos_stride;      // between batches (0: shared)
+    int pos0;                  // position of row 0 without a table
+};
+
+cudaError_t launch_rope(const RopeParams &p, bool bf16, int sms, cudaStream_t stream);
+
+// ------------------------------------------------------------- paged cache
+// The cache as the kernels see it: key t of sequence b lies in page
+// table[b][t / page_size], row t % page_size.
+struct PagedCache {
+    void *k, *v;
+    long long k_page, k_head, k_tok;    // strides in elements
+    long long v_page, v_head, v_tok;
+    const int *table;
+    long long table_stride;
+    const int *seq_lens;
+    int num_seqs, max_pages, num_pages, page_size, Hkv, D;
+};
+
+struct AppendParams {
+    PagedCache kv;
+    const void *k, *v;                  // [Hkv, T, D] new rows
+    long long k_h, k_n, v_h, v_n;
+    const void *q;                      // [H, T, D] or nullptr
+    void *q_out;
+    long long q_h, q_n, qo_h, qo_n;
+    int H;                              // query heads (0: no queries)
+    int T;
+    const int *cu;                      // [num_seqs + 1]
+    int rot, interleaved;               // rot 0: nothing is rotated
+    float scale;
+    const double *inv_freq;
+    const int *positions;               // [T] or nullptr (the cache position)
+};
+
+cudaError_t launch_paged_append(const AppendParams &p, bool bf16, int sms, cudaStream_t stream);
+
+// Sequence b of the batch: its first new row in the packed tensors, new rows
+// and keys, every table entry clamped so that no access can leave the tensors.
+struct PagedSeq {
+    int q0, new_q, len_k;
+};
+
+__host__ __device__ inline PagedSeq paged_seq(int b, const int *cu, const int *seq_lens, int total_q, int max_q,
+                                              long long capacity) {
+    PagedSeq s;
+    s.q0 = min(max(cu[b], 0), total_q);
+    s.new_q = min(max(cu[b + 1] - s.q0, 0), min(max_q, total_q - s.q0));
+    const long long len = seq_lens[b];
+    s.len_k = static_cast<int>(len < 0 ? 0 : (len < capacity ? len : capacity));
+    return s;
+}
+
+struct PagedFwdParams {
+    PagedCache kv;
+    const void *q;                      // [H, T, D]
+    long long q_h, q_n;
+    void *o;                            // [H, T, D]
+    long long o_h, o_n;
+    float *lse;                         // [H, T]
+    const int *cu;
+    int T, max_q, H, G;                 // G = H / Hkv
+    int causal;
+    float qk_scale_log2;
+    int *err;
+    unsigned long long timeout_ns;
+};
+
+cudaError_t launch_paged_fwd(const PagedFwdParams &p, bool bf16, int sms, cudaStream_t stream);
+
+}  // namespace fa

@@ -257,6 +257,134 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o,
                    int B, int H, int Nq, int Nk, int D, int causal, float scale,
                    int dtype, const float *key_bias, void *stream);
 
+/*
+ * Rotary positions.  A row x at position p has the pair (a, b) =
+ * (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) when interleaved, turned by
+ * theta = p * inv_freq[i], i < rot_dim/2:
+ *     a' = scale * (a cos theta - b sin theta)
+ *     b' = scale * (b cos theta + a sin theta)
+ * and its values [rot_dim, D) unchanged.
+ *   inv_freq     device float64 [rot_dim/2], 8-byte aligned: radians per
+ *                position, finite.  Scaled contexts are scaled frequencies.
+ *   rot_dim      a multiple of 16, 16 <= rot_dim <= D.
+ *   interleaved  0 or 1.
+ *   scale        multiplies cosine and sine (the attention factor of a scaling
+ *                rule; 1 otherwise); finite and > 0.
+ * The angle is reduced modulo a turn in 64-bit fixed point, so far positions
+ * lose nothing; the rest is float32, rounded once to the tensors' type.
+ */
+typedef struct fa_rope_spec {
+    const double *inv_freq;
+    int rot_dim;
+    int interleaved;
+    float scale;
+} fa_rope_spec;
+
+/*
+ * fa_rope: rotates q [B, Hq, N, D] and k [B, Hk, N, D] into q_out and k_out
+ * (same shapes) in one launch.  fa_rope_bwd: the gradient of that with respect
+ * to q and k -- the transposed rotation of dq_out, dk_out into dq, dk; neither
+ * positions nor frequencies receive one.
+ *   *_strides    HOST array of three: elements between batches, heads and
+ *                rows; D is contiguous.  Multiples of 8 (ignored where the
+ *                extent is 1); NULL = contiguous.  Outputs' rows must not
+ *                overlap.  Packed rows [H, total, D] are B = 1.
+ *   k            may be NULL with Hk = 0 (only q is rotated).
+ *   positions    device int32 [B, N] with pos_stride elements between batches
+ *                (0: one row for all), any sign; or NULL: row n is at
+ *                pos0 + n.
+ *   D            a multiple of 8, 16 <= D <= 512.
+ * An output may be its own input (the same pointer and strides).  B * N and
+ * B * N * D / 16 must fit in 31 bits.
+ */
+int fa_rope(const void *q, const long long *q_strides, void *q_out, const long long *q_out_strides,
+            int Hq, const void *k, const long long *k_strides, void *k_out,
+            const long long *k_out_strides, int Hk, int B, int N, int D,
+            const fa_rope_spec *rope, const int *positions, long long pos_stride, int pos0,
+            int dtype, void *stream);
+int fa_rope_bwd(const void *dq_out, const long long *dq_out_strides, void *dq,
+                const long long *dq_strides, int Hq, const void *dk_out,
+                const long long *dk_out_strides, void *dk, const long long *dk_strides, int Hk,
+                int B, int N, int D, const fa_rope_spec *rope, const int *positions,
+                long long pos_stride, int pos0, int dtype, void *stream);
+
+/*
+ * A paged key/value cache and the sequences that live in it.
+ *   k_cache, v_cache  device [num_pages, num_kv_heads, page_size, D] through
+ *                     k_strides, v_strides: elements between pages, heads and
+ *                     rows (D contiguous; multiples of 8 and at least D;
+ *                     ignored where the extent is 1).
+ *   page_table        device int32 [num_seqs, max_pages], table_stride
+ *                     elements between sequences: key t of sequence b is row
+ *                     t % page_size of page page_table[b][t / page_size].
+ *   seq_lens          device int32 [num_seqs]: keys of each sequence, the new
+ *                     ones of the current call included.
+ *   page_size         a multiple of 8, at most 65536; max_pages * page_size at
+ *                     most 2^30.
+ *   D, dtype          64 or 128; FA_F16 or FA_BF16.
+ * The tables are read on the device only.  Lengths are clamped to
+ * [0, max_pages * page_size]; a page index outside [0, num_pages) is never
+ * followed: what would be stored there is dropped and its keys and values
+ * read as zeros.  Entries past a sequence's last page are not read.
+ */
+typedef struct fa_paged_kv {
+    void *k_cache, *v_cache;
+    long long k_strides[3], v_strides[3];
+    const int *page_table;
+    long long table_stride;
+    const int *seq_lens;
+    int num_seqs, max_pages, num_pages, num_kv_heads, page_size, D, dtype;
+} fa_paged_kv;
+
+/*
+ * Appends the new rows of a ragged batch to the cache, before fa_paged_fwd()
+ * on the same stream.  Row t of the packed tensors belongs to the sequence b
+ * with cu_seqlens_q[b] <= t < cu_seqlens_q[b+1] (DEVICE int32 [num_seqs + 1],
+ * as in fa_fwd_varlen()); the new rows of b are its last ones, so row t is its
+ * key seq_lens[b] - cu_seqlens_q[b+1] + t.
+ *   k, v       [num_kv_heads, total_q, D], *_strides HOST arrays of two:
+ *              elements between heads and rows (as above).
+ *   rope       NULL, or the rotation of k (v is stored as it is).
+ *   positions  device int32 [total_q] for the rotation, or NULL: the key's
+ *              index in its sequence.
+ *   q, q_out   optional (both NULL with Hq = 0): [Hq, total_q, D] queries of the
+ *              same rows, rotated in the same launch (in place allowed).
+ *              Needs a rope.
+ * Rows of no sequence are neither read nor written.  Sequences must not share
+ * the pages that they write.
+ */
+int fa_paged_append(const fa_paged_kv *kv, const void *k, const long long *k_strides, const void *v,
+                    const long long *v_strides, const int *cu_seqlens_q, int total_q,
+                    const fa_rope_spec *rope, const int *positions, const void *q,
+                    const long long *q_strides, void *q_out, const long long *q_out_strides, int Hq,
+                    void *stream);
+
+/*
+ * Attention of a ragged batch of new rows over the paged cache, exact as in
+ * fa_fwd_varlen(): prompts, chunks of prompts, drafted tokens and single tokens
+ * in any mixture.
+ *   q, o       [Hq, total_q, D] with *_strides as in fa_paged_append(); Hq is a
+ *              multiple of num_kv_heads, at most 128 times it: head h reads kv
+ *              head h / (Hq / num_kv_heads).
+ *   lse        [Hq, total_q] float32.
+ *   max_seqlen_q  upper bound of the sequences' new rows (a longer one is cut at
+ *              the bound).
+ *   causal     1: bottom-right aligned within each sequence, row i of n new
+ *              ones sees the keys j <= i + seq_lens[b] - n.  0: all of them.
+ *   workspace  fa_paged_fwd_workspace_bytes() bytes, 16-byte aligned, owned by
+ *              the caller; contents on entry irrelevant, and calls that may
+ *              overlap need one each.
+ * Rows of the packed tensors that belong to no sequence are not written; a row
+ * that sees no key gets O = 0, LSE = -inf.  What the cache holds past a
+ * sequence's length (NaN included) does not matter.  The result does not
+ * depend on timing: the same call gives the same bits.
+ */
+size_t fa_paged_fwd_workspace_bytes(const fa_paged_kv *kv, int Hq, int max_seqlen_q);
+int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_strides, void *o,
+                 const long long *o_strides, float *lse, const int *cu_seqlens_q, int total_q,
+                 int max_seqlen_q, int Hq, int causal, float scale, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *fa_status_string(int status);
 
