@@ -5,101 +5,779 @@
 // over the keys j < len of row i's sequence, with causal also
 // j <= i + len - new; head h reads kv head h / G.
 //
-// One block per row and head, one thread per key of a 128-key step.
+// One pass over the keys with the running maximum and sum, on the tensor cores:
+// S = Q K^T and O += P V are tcgen05 products of 128 x 128 tiles with their
+// accumulators in tensor memory, K and V stream in by TMA, box by box as the
+// page table says.
+//
+// Rows.  The query heads of a group read the same keys, so a tile of 128 query
+// rows holds floor(128 / G) tokens times the G heads of one kv head (row =
+// token * G + head): a single token still shares its keys among its heads.  A
+// unit of work is up to two such tiles; how the units are shared out over the
+// CTAs is in fa_paged_sched.cuh.
+//
+// Jobs.  A job is one S product, its softmax and its P V product.  A unit of two
+// row tiles makes two jobs of each key tile; a unit of one row tile, one.  Jobs
+// alternate between two slots (S and O columns of tensor memory and a softmax
+// warpgroup each), so a unit of one row tile sends its even and odd key tiles
+// through different slots and adds the two results at its end: single tokens
+// keep both warpgroups and the tensor pipe busy too.  The tensor pipe runs
+// PV(q), S(q + 2) for job after job, across units.
+//
+// Warps: 0-3 and 4-7 softmax of slot 0 and 1 (a thread per row), 8 TMA (its
+// lanes look up a box's page each), 9 MMA, 10 walks the CTA's share of the work
+// and hands descriptors of its segments to the others through a ring.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_paged_internal.h"
+#include "fa_paged_sched.cuh"
+#include "fa_ptx.cuh"
 
 namespace fa {
 namespace {
 
+constexpr int kBM = 128;            // query rows per tile
+constexpr int kBN = 128;            // keys per tile
+constexpr int kThreads = 384;       // three warpgroups
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kPlanWarp = 10;
+// Register split (launch pool 168 x 384 = 64512 = 256 * 192 + 128 * 120).
+constexpr uint32_t kRegsSoftmax = 192;
+constexpr uint32_t kRegsOther = 120;
+constexpr int kDescs = 4;           // segment descriptors in the ring
+constexpr float kTau = 8.0f;        // lazy-rescale threshold (log2 units)
+constexpr int kEmuEvery = 4;        // one pair of exponentials in kEmuEvery on the FMA pipe
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A segment: key tiles [t0, t0 + nt) of a unit (nt == 0: the end of the work).
+struct Seg {
+    int row0, ntok;     // first row of the packed tensors, tokens
+    int h, b;           // kv head, sequence
+    int len_k, lim0;    // keys of the sequence; last key the first token sees
+    int t0, nt;
+    int two;            // two tiles of query rows
+    int tail;           // keys below len_k in the last key tile
+    int dest;           // -1: the rows' results, else partial result `dest` of this CTA
+    int pad;
+};
+
+template <int D>
+struct PagedLayout {
+    static constexpr int kStages = D == 64 ? 4 : 2;       // K and V tiles in flight each
+    static constexpr int kChunks = D / 64;                // 128-byte column blocks per row
+    static constexpr int kChunkBytes = kBN * 128;
+    static constexpr int kTileBytes = kChunks * kChunkBytes;
+    static constexpr int kQ = 0;                          // ring of two row tiles
+    static constexpr int kK = kQ + 2 * kTileBytes;
+    static constexpr int kV = kK + kStages * kTileBytes;
+    static constexpr int kBar = kV + kStages * kTileBytes;
+    static constexpr int kQFull = 0;                      // +buffer
+    static constexpr int kQEmpty = 2;
+    static constexpr int kSFull = 4;                      // +slot
+    static constexpr int kPHalf = 6;                      // +2 * slot + half
+    static constexpr int kOFull = 10;                     // +slot
+    static constexpr int kStat = 12;                      // statistics of both slots written
+    static constexpr int kRead = 13;                      // O of both slots read
+    static constexpr int kDrain = 14;
+    static constexpr int kDFull = 15;                     // +descriptor
+    static constexpr int kDEmpty = kDFull + kDescs;
+    static constexpr int kKFull = kDEmpty + kDescs;       // +stage
+    static constexpr int kKEmpty = kKFull + kStages;
+    static constexpr int kVFull = kKEmpty + kStages;
+    static constexpr int kVEmpty = kVFull + kStages;
+    static constexpr int kNumBars = kVEmpty + kStages;
+    static constexpr int kMisc = kBar + kNumBars * 8;     // tensor-memory base, abort flag
+    static constexpr int kDesc = (kMisc + 8 + 15) / 16 * 16;
+    static constexpr int kStats = kDesc + kDescs * static_cast<int>(sizeof(Seg));   // float2 [2][128]
+    static constexpr int kBytes = kStats + 2 * kBM * 8;
+    static constexpr int kAlloc = kBytes + 1024;          // room to align the base
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr uint32_t kColS = 0, kColO = 256;     // S of slot s at 128 s, O at 256 + D s
+    static_assert(kAlloc <= 232448, "shared memory");
+    static_assert(sizeof(Seg) % 16 == 0, "descriptors are copied as int4");
+};
+
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
 template <bool BF16>
-__device__ __forceinline__ float to_f(uint16_t x) {
-    if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(x) << 16);
-    else return __half2float(__ushort_as_half(x));
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    } else {
+        __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *a) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a[0]), "r"(a[1]),
+                 "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])
+                 : "memory");
+}
+
+// Rows without a visible key: O = 0, LSE = -inf.
+template <int D>
+__device__ __forceinline__ void write_empty(const PagedFwdParams &p, int row0, int ntok, int h, int lane) {
+    const int n = ntok * p.G;
+    for (int r = lane; r < n; r += 32) {
+        const int t = row0 + r / p.G, head = h * p.G + r % p.G;
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + head * p.o_h + t * p.o_n);
+        for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
+        p.lse[static_cast<long long>(head) * p.T + t] = neg_inf();
+    }
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) fa_paged_rows_kernel(const PagedFwdParams p) {
-    __shared__ float sq[D], sp[128], red[4];
-    const int t = blockIdx.x, h = blockIdx.y, hk = h / p.G, tid = threadIdx.x;
-    int b = 0;
-    for (int i = 0; i < p.kv.num_seqs; i += 128)
-        b += __syncthreads_count(i + tid < p.kv.num_seqs && p.cu[i + tid + 1] <= t);
-    if (b >= p.kv.num_seqs) return;
-    const PagedSeq s = paged_seq(b, p.cu, p.kv.seq_lens, p.T, p.max_q,
-                                 static_cast<long long>(p.kv.max_pages) * p.kv.page_size);
-    const int i = t - s.q0;
-    if (i < 0 || i >= s.new_q) return;
-    const int n = p.causal ? min(s.len_k, i + s.len_k - s.new_q + 1) : s.len_k;
-    const uint16_t *q = static_cast<const uint16_t *>(p.q) + h * p.q_h + t * p.q_n;
-    if (tid < D) sq[tid] = to_f<BF16>(q[tid]) * p.qk_scale_log2;
+__global__ void __launch_bounds__(kThreads, 1)
+fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedFwdParams p) {
+    using L = PagedLayout<D>;
+    constexpr int kStages = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PlanSmem plan_smem;
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
+    Seg *descs = reinterpret_cast<Seg *>(smem + L::kDesc);
+    float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(L::kQFull + i), 1);
+            mbar_init(bar(L::kQEmpty + i), 1);
+            mbar_init(bar(L::kSFull + i), 1);
+            mbar_init(bar(L::kPHalf + 2 * i), 4 * 32);
+            mbar_init(bar(L::kPHalf + 2 * i + 1), 4 * 32);
+            mbar_init(bar(L::kOFull + i), 1);
+        }
+        mbar_init(bar(L::kStat), 8 * 32);
+        mbar_init(bar(L::kRead), 8 * 32);
+        mbar_init(bar(L::kDrain), 1);
+        for (int i = 0; i < kDescs; ++i) {
+            mbar_init(bar(L::kDFull + i), 1);
+            mbar_init(bar(L::kDEmpty + i), 10);      // producer, MMA and eight softmax warps
+        }
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar(L::kKFull + s), 1);
+            mbar_init(bar(L::kKEmpty + s), 1);
+            mbar_init(bar(L::kVFull + s), 1);
+            mbar_init(bar(L::kVEmpty + s), 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    const Piece pc = plan_piece<kThreads>(p, p.geom, p.min_piece, plan_smem);
+    tc_fence_before();
     __syncthreads();
-    float m = neg_inf(), l = 0.f, acc = 0.f;
-    for (int j0 = 0; j0 < n; j0 += 128) {
-        const int j = j0 + tid;
-        float x = neg_inf();
-        if (j < n) {
-            const long long page = p.kv.table[b * p.kv.table_stride + j / p.kv.page_size];
-            x = 0.f;
-            if (page >= 0 && page < p.kv.num_pages) {
-                const uint16_t *k = static_cast<const uint16_t *>(p.kv.k) + page * p.kv.k_page + hk * p.kv.k_head +
-                                    (j % p.kv.page_size) * p.kv.k_tok;
-                for (int d = 0; d < D; ++d) x = fmaf(sq[d], to_f<BF16>(k[d]), x);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wctx{p.timeout_ns, p.err, abort_flag};
+    // Descriptor u, by a whole warp; each warp arrives on its "empty" barrier
+    // when it has taken what it needs.
+    auto desc_wait = [&](int u) -> bool {
+        return mbar_wait_warp(bar(L::kDFull + u % kDescs), (u / kDescs) & 1, wctx);
+    };
+    auto desc_release = [&](int u) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kDEmpty + u % kDescs));
+    };
+    // Nobody asks for registers again after the split, so it cannot deadlock;
+    // every role ends at the CTA barrier 1, and the MMA warp frees tensor memory
+    // after it.
+    if (warp >= 8) regs_release<kRegsOther>();
+    if (warp == kPlanWarp) {
+        // ===================== the CTA's share of the work =====================
+        MergeMeta mm{0, 0, 0, -1};
+        if (pc.b >= 0) {
+            bool ok = true;
+            int u = 0;
+            auto push = [&](const Seg &s) -> bool {
+                const int i = u % kDescs;
+                if (u >= kDescs && !mbar_wait_warp(bar(L::kDEmpty + i), ((u / kDescs) - 1) & 1, wctx)) return false;
+                if (lane == 0) {
+                    descs[i] = s;
+                    mbar_arrive(bar(L::kDFull + i));
+                }
+                ++u;
+                return true;
+            };
+            SegWalk w;
+            w.first(p, p.geom, pc);
+            do {
+                const int ntok = min(p.geom.unit_tokens, w.s.new_q - w.tok0), row0 = w.s.q0 + w.tok0;
+                if (w.n == 0) {
+                    write_empty<D>(p, row0, ntok, w.h, lane);
+                } else if (!w.none()) {
+                    Seg s;
+                    s.row0 = row0;
+                    s.ntok = ntok;
+                    s.h = w.h;
+                    s.b = w.b;
+                    s.len_k = w.s.len_k;
+                    s.lim0 = w.tok0 + w.s.len_k - w.s.new_q;
+                    s.t0 = w.t0;
+                    s.nt = w.t1 - w.t0;
+                    s.two = w.two;
+                    s.tail = min(kBN, w.s.len_k - (w.t1 - 1) * kBN);
+                    s.dest = w.whole() ? -1 : (w.t0 == 0 ? 1 : 0);
+                    s.pad = 0;
+                    if (w.t0 == 0 && w.t1 < w.n) mm = MergeMeta{row0, ntok, w.h, w.last_cta(pc)};
+                    ok = push(s);
+                }
+            } while (ok && w.next(p, p.geom));
+            if (ok) {
+                Seg s{};
+                push(s);
             }
         }
-        float mx = x;
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        const float e = mn == neg_inf() ? 0.f : exp2f(x - mn);
-        sp[tid] = e;
-        float sum = e;
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = sum;
-        __syncthreads();
-        const float alpha = m == neg_inf() ? 0.f : exp2f(m - mn);
-        l = l * alpha + ((red[0] + red[1]) + (red[2] + red[3]));
-        m = mn;
-        acc *= alpha;
-        if (tid < D) {
-            for (int jj = 0; jj < min(128, n - j0); ++jj) {
-                const long long page = p.kv.table[b * p.kv.table_stride + (j0 + jj) / p.kv.page_size];
-                if (page < 0 || page >= p.kv.num_pages) continue;
-                acc = fmaf(sp[jj], to_f<BF16>(static_cast<const uint16_t *>(p.kv.v)[page * p.kv.v_page + hk * p.kv.v_head +
-                                                                                    ((j0 + jj) % p.kv.page_size) * p.kv.v_tok + tid]), acc);
+        if (lane == 0) p.meta[blockIdx.x] = mm;
+        named_bar_sync(1, kThreads);
+    } else if (pc.b < 0) {
+        named_bar_sync(1, kThreads);
+        if (warp == kMmaWarp) {
+            __syncwarp();
+            tmem_dealloc(tmem, L::kTmemCols);
+        }
+    } else if (warp == kProducerWarp) {
+        // ===================== TMA producer =====================
+        const int boxes = kBN / p.box;
+        const int lane_box = lane / L::kChunks, lane_chunk = lane % L::kChunks;
+        const bool copies = lane_box < boxes;
+        const uint32_t dst = lane_chunk * L::kChunkBytes + lane_box * p.box * 128;
+        const uint32_t q_bytes = static_cast<uint32_t>(L::kChunks * 128 * p.G * p.geom.tile_tokens);
+        int t = 0;          // key tiles begun so far (ring position)
+        int k_n = 0, v_n = 0, q_n = 0;      // copies issued
+        bool ok = true;
+        for (int u = 0; ok; ++u) {
+            if (!desc_wait(u)) { ok = false; break; }
+            const Seg s = descs[u % kDescs];
+            desc_release(u);
+            if (s.nt == 0) break;
+            // this lane's page and row of key tile kt (a page that is not to be
+            // read: one past the last, which TMA fills with zeros)
+            const int *table = p.kv.table + s.b * p.kv.table_stride;
+            int page = 0, row = 0;
+            auto look_up = [&](int kt) {
+                const int key = kt * kBN + lane_box * p.box;
+                page = p.kv.num_pages;
+                row = 0;
+                if (copies && key < s.len_k) {
+                    const int pi = key / p.kv.page_size;
+                    row = key - pi * p.kv.page_size;
+                    const int g = __ldg(table + pi);
+                    if (g >= 0 && g < p.kv.num_pages) page = g;
+                }
+            };
+            look_up(s.t0);
+            for (int i = 0; i <= s.two && ok; ++i, ++q_n) {
+                const int bf = q_n & 1;
+                if (!mbar_wait_warp(bar(L::kQEmpty + bf), ((q_n >> 1) & 1) ^ 1, wctx)) { ok = false; break; }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(L::kQFull + bf), q_bytes);
+#pragma unroll
+                    for (int c = 0; c < L::kChunks; ++c)
+                        tma_load_3d(sbase + L::kQ + bf * L::kTileBytes + c * L::kChunkBytes, &tm_q,
+                                    bar(L::kQFull + bf), c * 64, s.h * p.G, s.row0 + i * p.geom.tile_tokens);
+                }
+            }
+            for (int j = 0; j < s.nt && ok; ++j, ++t) {
+                const int st = t % kStages;
+                const uint32_t ph = (t / kStages) & 1;
+                const int pg = page, rw = row;
+                if (!mbar_wait_warp(bar(L::kKEmpty + st), ph ^ 1, wctx)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(bar(L::kKFull + st), L::kTileBytes);
+                __syncwarp();
+                if (copies)
+                    tma_load_4d(sbase + L::kK + st * L::kTileBytes + dst, &tm_k, bar(L::kKFull + st), lane_chunk * 64,
+                                rw, s.h, pg);
+                ++k_n;
+                if (j + 1 < s.nt) look_up(s.t0 + j + 1);
+                if (!mbar_wait_warp(bar(L::kVEmpty + st), ph ^ 1, wctx)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(bar(L::kVFull + st), L::kTileBytes);
+                __syncwarp();
+                if (copies)
+                    tma_load_4d(sbase + L::kV + st * L::kTileBytes + dst, &tm_v, bar(L::kVFull + st), lane_chunk * 64,
+                                rw, s.h, pg);
+                ++v_n;
             }
         }
-        __syncthreads();
+        if (!ok) {
+            // bounded chance for the copies in flight to land before the CTA's
+            // shared memory goes away
+            volatile int zero = 0;
+            const WaitCtx drain{wctx.timeout_ns, wctx.err, &zero};
+            for (int i = max(0, q_n - 2); i < q_n; ++i) mbar_wait(bar(L::kQFull + (i & 1)), (i >> 1) & 1, drain);
+            for (int i = max(0, k_n - kStages); i < k_n; ++i)
+                mbar_wait(bar(L::kKFull + i % kStages), (i / kStages) & 1, drain);
+            for (int i = max(0, v_n - kStages); i < v_n; ++i)
+                mbar_wait(bar(L::kVFull + i % kStages), (i / kStages) & 1, drain);
+        }
+        __syncwarp();
+        named_bar_sync(1, kThreads);
+    } else if (warp == kMmaWarp) {
+        // ============ MMA issuer (whole warp; one elected lane issues) ============
+        constexpr uint32_t idesc_qk = idesc_f16_f32acc(BF16, kBM, kBN, false, false);
+        constexpr uint32_t idesc_pv = idesc_f16_f32acc(BF16, kBM, D, false, true);
+        struct Cursor {
+            int u = 0, j = 0, g = 0, t = 0;     // segment, its job, jobs and key tiles so far
+            int jobs = 0, two = 0, tail = kBN;
+        };
+        bool ok = true, any = false;
+        auto enter = [&](Cursor &c) -> bool {   // the cursor's segment; jobs == 0: the end
+            if (!desc_wait(c.u)) return false;
+            const Seg &s = descs[c.u % kDescs];
+            c.two = s.two;
+            c.jobs = s.two ? 2 * s.nt : s.nt;
+            c.tail = s.tail;
+            c.j = 0;
+            return true;
+        };
+        Cursor cs, cp;
+        int q_n = 0;            // row tiles taken so far
+        // S of the next job: into the S columns of slot g & 1
+        auto step_s = [&]() -> bool {
+            if (cs.jobs == 0) return true;
+            const int slot = cs.g & 1, st = cs.t % kStages;
+            const int qi = cs.two ? (cs.j & 1) : 0;
+            const int bf = (q_n + qi) & 1;
+            if (cs.j <= cs.two && !mbar_wait_warp(bar(L::kQFull + bf), ((q_n + qi) >> 1) & 1, wctx)) return false;
+            if (!mbar_wait_warp(bar(L::kKFull + st), (cs.t / kStages) & 1, wctx)) return false;
+            tc_fence_after();
+            const bool tile_done = !cs.two || (cs.j & 1);
+            const uint64_t dq = smem_desc_sw128(sbase + L::kQ + bf * L::kTileBytes, 16, 1024);
+            const uint64_t dk = smem_desc_sw128(sbase + L::kK + st * L::kTileBytes, 16, 1024);
+            const uint32_t d = tmem + L::kColS + slot * 128;
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
+                    umma_f16_ss(d, dq + off, dk + off, idesc_qk, kk > 0);
+                }
+                umma_commit(bar(L::kSFull + slot));
+                if (tile_done) umma_commit(bar(L::kKEmpty + st));
+                if (cs.j + 1 + cs.two >= cs.jobs) umma_commit(bar(L::kQEmpty + bf));
+            }
+            __syncwarp();
+            any = true;
+            if (tile_done) ++cs.t;
+            ++cs.g;
+            if (++cs.j == cs.jobs) {
+                q_n += 1 + cs.two;
+                ++cs.u;
+                return enter(cs);
+            }
+            return true;
+        };
+        ok = enter(cs);
+        cp = cs;
+        for (int i = 0; i < 2 && ok; ++i) ok = step_s();
+        while (ok && cp.jobs > 0) {
+            // ---- P V of the oldest job, half by half
+            const int slot = cp.g & 1, st = cp.t % kStages;
+            const uint32_t pp = (cp.g >> 1) & 1;
+            if (!mbar_wait_warp(bar(L::kVFull + st), (cp.t / kStages) & 1, wctx)) { ok = false; break; }
+            if (cp.tail < kBN && cp.j >= cp.jobs - 1 - cp.two && (!cp.two || !(cp.j & 1))) {
+                // the sequence ends inside this key tile: P is 0 past it, but the
+                // cache may hold anything there (NaN), so V is made 0 too
+                const int n = (kBN - cp.tail) * 8;
+                for (int c = 0; c < L::kChunks; ++c) {
+                    uint4 *z = reinterpret_cast<uint4 *>(smem + L::kV + st * L::kTileBytes + c * L::kChunkBytes +
+                                                         cp.tail * 128);
+                    for (int e = lane; e < n; e += 32) z[e] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            const uint64_t dv = smem_desc_sw128(sbase + L::kV + st * L::kTileBytes, L::kChunkBytes, 1024);
+            const uint32_t pa = tmem + L::kColS + slot * 128;
+            const uint32_t d = tmem + L::kColO + slot * D;
+            const bool acc = cp.j >= 2;
+            for (int h = 0; h < 2; ++h) {
+                if (!mbar_wait_warp(bar(L::kPHalf + 2 * slot + h), pp, wctx)) { ok = false; break; }
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ts(d, pa + (4 * h + kk) * 8, dv + ((static_cast<uint32_t>(4 * h + kk) * 16 * 128) >> 4),
+                                    idesc_pv, acc || h + kk > 0);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            const bool tile_done = !cp.two || (cp.j & 1);
+            if (elect_one()) {
+                if (tile_done) umma_commit(bar(L::kVEmpty + st));
+                if (cp.j + 2 >= cp.jobs) umma_commit(bar(L::kOFull + slot));
+            }
+            __syncwarp();
+            if (tile_done) ++cp.t;
+            ++cp.g;
+            if (++cp.j == cp.jobs) {
+                desc_release(cp.u);
+                ++cp.u;
+                if (!step_s() || !enter(cp)) { ok = false; break; }
+            } else if (!step_s()) {
+                ok = false;
+                break;
+            }
+        }
+        if (any) {
+            // every issued MMA must finish before tensor memory is released
+            if (elect_one()) umma_commit(bar(L::kDrain));
+            __syncwarp();
+            volatile int zero = 0;
+            const WaitCtx drain{wctx.timeout_ns, wctx.err, &zero};
+            mbar_wait(bar(L::kDrain), 0, drain);
+        }
+        __syncwarp();
+        named_bar_sync(1, kThreads);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, L::kTmemCols);
+    } else if (warp < 8) {
+        // ===================== softmax warpgroups =====================
+        regs_alloc<kRegsSoftmax>();
+        const int slot = warp >> 2;
+        const int wq = warp & 3;            // lane quarter of tensor memory
+        const int row = wq * 32 + lane;     // row within the tile
+        const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        const uint32_t tS = tl + L::kColS + slot * 128;
+        const float qk = p.qk_scale_log2;
+        const int r_tok = row / p.G, r_head = row - r_tok * p.G;
+        bool ok = true;
+        int g0 = 0;                         // jobs before this segment
+        int o_n0 = 0, o_n1 = 0;             // segments that used slot 0 and 1
+        int merges = 0;
+        for (int u = 0;; ++u) {
+            if (!desc_wait(u)) break;
+            const Seg s = descs[u % kDescs];
+            desc_release(u);
+            if (s.nt == 0) break;
+            const int jobs = s.two ? 2 * s.nt : s.nt;
+            const int first = (slot ^ g0) & 1;              // this slot's first job
+            const uint32_t o_ph[2] = {static_cast<uint32_t>(o_n0 & 1), static_cast<uint32_t>(o_n1 & 1)};
+            if (jobs > 1) {
+                ++o_n0;
+                ++o_n1;
+            } else if (g0 & 1) {
+                ++o_n1;
+            } else {
+                ++o_n0;
+            }
+            if (first >= jobs) {                            // a single job, the other slot's
+                g0 += jobs;
+                continue;
+            }
+            const int qt = s.two ? first : 0;               // row tile
+            const int tok = qt * p.geom.tile_tokens + r_tok;
+            const bool valid = r_tok < p.geom.tile_tokens && tok < s.ntok;
+            const bool active = __any_sync(0xffffffffu, valid);
+            const int lim = p.causal ? min(s.lim0 + tok, s.len_k - 1) : s.len_k - 1;
+            // rows of nothing keep a finite reference maximum; what they compute is not used
+            float m_ref = valid ? neg_inf() : 0.f;          // log2 units
+            float l = 0.f;
+            for (int j = first; j < jobs; j += 2) {
+                const int kv0 = (s.t0 + (s.two ? j >> 1 : j)) * kBN;
+                {
+                    const bool got = mbar_wait(bar(L::kSFull + slot), ((g0 + j) >> 1) & 1, wctx);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                }
+                tc_fence_after();
+                if (!active) {
+                    tc_fence_before();
+                    mbar_arrive(bar(L::kPHalf + 2 * slot));
+                    mbar_arrive(bar(L::kPHalf + 2 * slot + 1));
+                    continue;
+                }
+                uint32_t sr[128];
+                tmem_ld32dp_x128_wait(tS, sr);
+                float x[128];
+#pragma unroll
+                for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c]);
+                if (kv0 + kBN - 1 > lim) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (kv0 + c > lim) x[c] = neg_inf();
+                }
+                float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+                for (int c = 4; c < 124; c += 8) {
+                    mx0 = fmax3(mx0, x[c], x[c + 1]);
+                    mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
+                    mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
+                    mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
+                }
+                const float m_tile =
+                    qk * fmax3(fmax3(mx0, mx1, x[124]), fmax3(mx2, mx3, x[125]), fmaxf(x[126], x[127]));
+                const bool need = valid && m_tile > m_ref + kTau;
+                const bool rescale = __any_sync(0xffffffffu, need);     // warp-uniform
+                float alpha = 1.f;
+                if (rescale) {
+                    const float m_new = need ? m_tile : m_ref;
+                    alpha = (m_ref == neg_inf()) ? 0.f : ex2_approx(m_ref - m_new);
+                    l *= alpha;
+                    m_ref = m_new;
+                }
+                const float m_use = (m_ref == neg_inf()) ? 0.f : m_ref;
+                // p = 2^(x - m) in two halves of 64 keys, each handed to the MMA
+                // warp on its own barrier; one pair in kEmuEvery on the FMA pipe
+                // once every row has a finite reference maximum (exp2_fma2 gives
+                // 2^-126 for a masked score, nothing next to l >= 1)
+                float2 lsum = make_float2(0.f, 0.f), lsum2 = make_float2(0.f, 0.f);
+                const float2 neg_m2 = make_float2(-m_use, -m_use);
+                const float2 qk2 = make_float2(qk, qk);
+                const bool emu = __all_sync(0xffffffffu, m_ref != neg_inf());
+                auto half = [&](int h, auto emu_tag) {
+                    constexpr bool kEmu = decltype(emu_tag)::value;
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c2 = 0; c2 < 32; ++c2) {
+                        const int c = 64 * h + 2 * c2;
+                        const float2 a = __ffma2_rn(make_float2(x[c], x[c + 1]), qk2, neg_m2);
+                        float2 pp;
+                        if (kEmu && c2 % kEmuEvery == kEmuEvery - 1)
+                            pp = exp2_fma2(a);
+                        else
+                            pp = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+                        if (c2 & 1)
+                            lsum2 = __fadd2_rn(lsum2, pp);
+                        else
+                            lsum = __fadd2_rn(lsum, pp);
+                        pk[c2] = pack2<BF16>(pp.x, pp.y);
+                    }
+                    tmem_st32dp_x32(tS + 32 * h, pk);
+                };
+                if (emu)
+                    half(0, std::true_type{});
+                else
+                    half(0, std::false_type{});
+                if (rescale && j > 1) {
+                    // O row *= alpha.  O is stable: this S tile's MMA was issued
+                    // after the slot's previous P V and its commit covers it.
+                    const uint32_t tO = tl + L::kColO + slot * D;
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t orr[32];
+                        tmem_ld32dp_x32_wait(tO + cc * 32, orr);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                        tmem_st32dp_x32(tO + cc * 32, orr);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(L::kPHalf + 2 * slot));
+                if (emu)
+                    half(1, std::true_type{});
+                else
+                    half(1, std::false_type{});
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(L::kPHalf + 2 * slot + 1));
+                l += (lsum.x + lsum.y) + (lsum2.x + lsum2.y);
+            }
+            if (!ok) break;
+
+            // ---- the rows' results: O = o / l, LSE = (m_ref + log2 l) ln 2
+            const int ur = tok * p.G + r_head;              // row of the unit
+            const int t = s.row0 + tok, head = s.h * p.G + r_head;
+            uint16_t *o_row = nullptr;
+            float *part = nullptr;
+            if (s.dest < 0)
+                o_row = static_cast<uint16_t *>(p.o) + head * p.o_h + t * p.o_n;
+            else
+                part = p.o_part + ((2 * blockIdx.x + s.dest) * static_cast<size_t>(p.part_rows) + ur) * D;
+            auto store = [&](int col, const float (&y)[32]) {
+                if (!valid) return;
+                if (s.dest < 0) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(y[2 * e], y[2 * e + 1]);
+                    if (p.o_v8) {
+                        st_global_v8(o_row + col, pk);
+                        st_global_v8(o_row + col + 16, pk + 8);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4 *>(o_row + col)[e] =
+                                make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        reinterpret_cast<float4 *>(part + col)[e] =
+                            make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                }
+            };
+            auto store_lse = [&](float m, float sum) {
+                if (!valid) return;
+                const float lse2 = sum > 0.f ? m + lg2_approx(sum) : neg_inf();
+                if (s.dest < 0)
+                    p.lse[static_cast<long long>(head) * p.T + t] = lse2 * kLn2;
+                else
+                    p.lse_part[(2 * blockIdx.x + s.dest) * static_cast<size_t>(p.part_rows) + ur] = lse2;
+            };
+            if (s.two || jobs == 1) {
+                const bool got = mbar_wait(bar(L::kOFull + slot), o_ph[slot], wctx);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                tc_fence_after();
+                if (active) {
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t r[32];
+                        tmem_ld32dp_x32_wait(tl + L::kColO + slot * D + cc * 32, r);
+                        float y[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(r[e]) * inv;
+                        store(32 * cc, y);
+                    }
+                    store_lse(m_ref, l);
+                }
+                tc_fence_before();
+            } else {
+                // the two slots hold the sums over the even and odd key tiles of
+                // the same rows; each warpgroup adds up half of the columns
+                stats[slot * kBM + row] = make_float2(m_ref, l);
+                mbar_arrive(bar(L::kStat));
+                bool got = mbar_wait(bar(L::kStat), merges & 1, wctx) && mbar_wait(bar(L::kOFull + 0), o_ph[0], wctx) &&
+                           mbar_wait(bar(L::kOFull + 1), o_ph[1], wctx);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                tc_fence_after();
+                if (active) {
+                    const float2 other = stats[(slot ^ 1) * kBM + row];
+                    const float m = fmaxf(m_ref, other.x);
+                    const float a = m_ref == neg_inf() ? 0.f : ex2_approx(m_ref - m);
+                    const float b = other.x == neg_inf() ? 0.f : ex2_approx(other.x - m);
+                    const float sum = l * a + other.y * b;
+                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    const float w_own = a * inv, w_oth = b * inv;
+#pragma unroll
+                    for (int cc = 0; cc < D / 64; ++cc) {
+                        const int col = slot * (D / 2) + 32 * cc;
+                        uint32_t r[32], q[32];
+                        tmem_ld32dp_x32_wait(tl + L::kColO + slot * D + col, r);
+                        tmem_ld32dp_x32_wait(tl + L::kColO + (slot ^ 1) * D + col, q);
+                        float y[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            y[e] = fmaf(__uint_as_float(r[e]), w_own, __uint_as_float(q[e]) * w_oth);
+                        store(col, y);
+                    }
+                    if (slot == 0) store_lse(m, sum);
+                }
+                // both read the other's O and statistics before either is replaced
+                tc_fence_before();
+                mbar_arrive(bar(L::kRead));
+                got = mbar_wait(bar(L::kRead), merges & 1, wctx);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                ++merges;
+            }
+            g0 += jobs;
+        }
+        __syncwarp();
+        named_bar_sync(1, kThreads);
+    } else {
+        named_bar_sync(1, kThreads);    // warp 11
     }
-    if (tid < D) {
-        const float r = l > 0.f ? acc / l : 0.f;
-        uint16_t *o = static_cast<uint16_t *>(p.o) + h * p.o_h + t * p.o_n;
-        if constexpr (BF16) o[tid] = __bfloat16_as_ushort(__float2bfloat16_rn(r));
-        else o[tid] = __half_as_ushort(__float2half_rn(r));
+}
+
+// Joins the partial results of the units that were cut: CTA c begins such a
+// unit (its partial result 1), CTAs c + 1 .. last continue it (their partial
+// results 0); added in that order.  One warp per row.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedFwdParams p) {
+    constexpr int kPer = D / 32;
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int ur = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const MergeMeta mm = p.meta[c];
+    if (mm.last < 0 || ur >= mm.tokens * p.G) return;
+    auto index = [&](int i) -> size_t {
+        return static_cast<size_t>(i == c ? 2 * c + 1 : 2 * i) * p.part_rows + ur;
+    };
+    float m = neg_inf();
+    for (int i = c + lane; i <= mm.last; i += 32) m = fmaxf(m, p.lse_part[index(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[kPer], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    if (m != neg_inf()) {
+#pragma unroll 4
+        for (int i = c; i <= mm.last; ++i) {
+            const float w = ex2_approx(p.lse_part[index(i)] - m);   // -inf: 0
+            const float *src = p.o_part + index(i) * D + lane * kPer;
+            sum += w;
+            if constexpr (kPer == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src);
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+                acc[2] = fmaf(w, v.z, acc[2]);
+                acc[3] = fmaf(w, v.w, acc[3]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(src);
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+            }
+        }
     }
-    if (tid == 0)
-        p.lse[static_cast<long long>(h) * p.T + t] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : neg_inf();
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int t = mm.row0 + ur / p.G, head = mm.h * p.G + ur % p.G;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + head * p.o_h + t * p.o_n + lane * kPer);
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) dst[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0)
+        p.lse[static_cast<long long>(head) * p.T + t] = sum > 0.f ? (m + lg2_approx(sum)) * kLn2 : neg_inf();
+}
+
+template <int D, bool BF16>
+cudaError_t launch_t(const PagedTensorMaps &tm, const PagedFwdParams &p, int grid, cudaStream_t stream) {
+    auto kern = fa_paged_kernel<D, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PagedLayout<D>::kAlloc);
+    if (e != cudaSuccess) return e;
+    prof_begin(stream, "fa_paged_kernel");
+    kern<<<grid, kThreads, PagedLayout<D>::kAlloc, stream>>>(tm.q, tm.k, tm.v, p);
+    prof_end(stream);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    prof_begin(stream, "fa_paged_merge_kernel");
+    fa_paged_merge_kernel<D, BF16><<<dim3(grid, (p.part_rows + 7) / 8), 256, 0, stream>>>(p);
+    prof_end(stream);
+    note_launch();
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_paged_fwd(const PagedFwdParams &p, bool bf16, int sms, cudaStream_t stream) {
-    (void)sms;
-    const dim3 grid(p.T, p.H);
-    auto kern = p.kv.D == 64 ? (bf16 ? fa_paged_rows_kernel<64, true> : fa_paged_rows_kernel<64, false>)
-                             : (bf16 ? fa_paged_rows_kernel<128, true> : fa_paged_rows_kernel<128, false>);
-    prof_begin(stream, "fa_paged_rows_kernel");
-    kern<<<grid, 128, 0, stream>>>(p);
-    prof_end(stream);
-    note_launch();
-    return cudaGetLastError();
+cudaError_t launch_paged_fwd(const PagedTensorMaps &tm, const PagedFwdParams &p, bool bf16, int sms,
+                             cudaStream_t stream) {
+    const int grid = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
+    if (p.kv.D == 64) return bf16 ? launch_t<64, true>(tm, p, grid, stream) : launch_t<64, false>(tm, p, grid, stream);
+    return bf16 ? launch_t<128, true>(tm, p, grid, stream) : launch_t<128, false>(tm, p, grid, stream);
 }
 
 }  // namespace fa

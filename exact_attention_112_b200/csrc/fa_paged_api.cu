@@ -3,8 +3,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "fa.h"
 #include "fa_host.h"
@@ -124,6 +126,44 @@ int check_cache(const fa_paged_kv *kv, fa::PagedCache *c) {
     return FA_OK;
 }
 
+// Shape of the work of a call: how many tokens make a tile of 128 query rows
+// (a token has G rows, one per head of the group) and a unit of two tiles.
+fa::SchedGeom sched_geom(int G, int max_q) {
+    fa::SchedGeom g;
+    g.tile = 128;
+    g.tile_tokens = std::max(1, std::min(128 / G, max_q));
+    g.unit_tokens = std::max(1, std::min(2 * (128 / G), max_q));
+    return g;
+}
+
+struct PagedWorkspace {
+    size_t lse, meta, bytes;    // offsets of the parts after the partial rows
+};
+
+PagedWorkspace paged_workspace(const fa::SchedGeom &g, int G, int D) {
+    const size_t rows = static_cast<size_t>(2) * fa::kPagedMaxCtas * g.unit_tokens * G;
+    PagedWorkspace w;
+    w.lse = rows * D * sizeof(float);
+    w.meta = w.lse + (rows * sizeof(float) + 15) / 16 * 16;
+    w.bytes = w.meta + fa::kPagedMaxCtas * sizeof(fa::MergeMeta);
+    return w;
+}
+
+int encode(CUtensorMap *m, const void *ptr, bool bf16, int rank, const cuuint64_t *dims, const long long *strides,
+           const cuuint32_t *box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    const int st = fa::host_encoder(&enc);
+    if (st != FA_OK) return st;
+    cuuint64_t bytes[4];
+    for (int i = 0; i + 1 < rank; ++i) bytes[i] = static_cast<cuuint64_t>(strides[i]) * 2;
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    const CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                           const_cast<void *>(ptr), dims, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -191,7 +231,7 @@ int fa_paged_append(const fa_paged_kv *kv, const void *k, const long long *k_str
 size_t fa_paged_fwd_workspace_bytes(const fa_paged_kv *kv, int Hq, int max_seqlen_q) {
     fa::PagedCache c;
     if (check_cache(kv, &c) != FA_OK || Hq < 1 || Hq % c.Hkv != 0 || Hq / c.Hkv > 128 || max_seqlen_q < 0) return 0;
-    return 256;
+    return paged_workspace(sched_geom(Hq / c.Hkv, max_seqlen_q), Hq / c.Hkv, c.D).bytes;
 }
 
 int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_strides, void *o,
@@ -211,24 +251,52 @@ int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_stride
     const long long n[2] = {Hq, total_q};
     long long s[2];
     if ((st = get_strides(q_strides, n, kv->D, kv->D, s)) != FA_OK) return st;
-    p.q_h = s[0]; p.q_n = s[1];
+    const long long q_h = s[0], q_n = s[1];
     if ((st = get_strides(o_strides, n, kv->D, kv->D, s)) != FA_OK) return st;
     p.o_h = s[0]; p.o_n = s[1];
     if (!workspace || workspace_bytes < fa_paged_fwd_workspace_bytes(kv, Hq, max_seqlen_q)) return FA_ERR_WORKSPACE;
-    p.q = q;
+    const int G = Hq / kv->num_kv_heads, D = kv->D;
+    const bool bf16 = kv->dtype == FA_BF16;
     p.o = o;
     p.lse = lse;
     p.cu = cu_seqlens_q;
     p.T = total_q;
     p.max_q = max_seqlen_q < total_q ? max_seqlen_q : total_q;
     p.H = Hq;
-    p.G = Hq / kv->num_kv_heads;
+    p.G = G;
     p.causal = causal;
     p.qk_scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    p.geom = sched_geom(G, p.max_q);
+    // a CTA takes two key tiles at least (it works on two at a time)
+    p.min_piece = p.geom.unit_tokens > p.geom.tile_tokens ? 4 : 2;
+    p.box = std::gcd(kv->page_size, 128);
+    p.o_v8 = aligned(o, 32) && p.o_h % 16 == 0 && p.o_n % 16 == 0;
+    p.part_rows = p.geom.unit_tokens * G;
+    const PagedWorkspace w = paged_workspace(p.geom, G, D);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.o_part = reinterpret_cast<float *>(ws);
+    p.lse_part = reinterpret_cast<float *>(ws + w.lse);
+    p.meta = reinterpret_cast<fa::MergeMeta *>(ws + w.meta);
     int sms = 1;
     if ((st = fa::host_device(&p.err, &sms)) != FA_OK) return st;
     p.timeout_ns = fa::host_wait_limit_ns();
-    return fa::launch_paged_fwd(p, kv->dtype == FA_BF16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    fa::PagedTensorMaps tm;
+    {   // rows in the order (token, head of the group): a box is a tile of query rows
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                                    static_cast<cuuint64_t>(total_q)};
+        const long long str[2] = {q_h, q_n};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(p.geom.tile_tokens)};
+        if ((st = encode(&tm.q, q, bf16, 3, dims, str, box)) != FA_OK) return st;
+    }
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(kv->page_size),
+                                    static_cast<cuuint64_t>(kv->num_kv_heads), static_cast<cuuint64_t>(kv->num_pages)};
+        const long long str[3] = {i ? p.kv.v_tok : p.kv.k_tok, i ? p.kv.v_head : p.kv.k_head,
+                                  i ? p.kv.v_page : p.kv.k_page};
+        const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.box), 1, 1};
+        if ((st = encode(i ? &tm.v : &tm.k, i ? p.kv.v : p.kv.k, bf16, 4, dims, str, box)) != FA_OK) return st;
+    }
+    return fa::launch_paged_fwd(tm, p, bf16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -82,10 +82,23 @@ __host__ __device__ inline PagedSeq paged_seq(int b, const int *cu, const int *s
     return s;
 }
 
+// Shape of the work units (fa_paged_sched.cuh).
+struct SchedGeom {
+    int tile;           // keys per tile
+    int unit_tokens;    // tokens per unit
+    int tile_tokens;    // tokens per tile of query rows (a unit past it counts double)
+};
+
+// What the merge kernel reads of CTA c: the unit that c begins and does not
+// end (last < 0: none).
+struct MergeMeta {
+    int row0, tokens, h, last;
+};
+
+constexpr int kPagedMaxCtas = 148;      // CTAs that share the work (partial results: two each)
+
 struct PagedFwdParams {
     PagedCache kv;
-    const void *q;                      // [H, T, D]
-    long long q_h, q_n;
     void *o;                            // [H, T, D]
     long long o_h, o_n;
     float *lse;                         // [H, T]
@@ -93,10 +106,23 @@ struct PagedFwdParams {
     int T, max_q, H, G;                 // G = H / Hkv
     int causal;
     float qk_scale_log2;
+    SchedGeom geom;
+    int min_piece;                      // least entries worth a CTA
+    int box;                            // keys per TMA box: gcd(page_size, 128)
+    int o_v8;                           // rows of o start 32-byte aligned
+    int part_rows;                      // rows of a partial result: unit_tokens * G
+    float *o_part;                      // [2 * kPagedMaxCtas, part_rows, D]
+    float *lse_part;                    // [2 * kPagedMaxCtas, part_rows], base-2
+    MergeMeta *meta;                    // [kPagedMaxCtas]
     int *err;
     unsigned long long timeout_ns;
 };
 
-cudaError_t launch_paged_fwd(const PagedFwdParams &p, bool bf16, int sms, cudaStream_t stream);
+struct PagedTensorMaps {
+    CUtensorMap q, k, v;
+};
+
+cudaError_t launch_paged_fwd(const PagedTensorMaps &tm, const PagedFwdParams &p, bool bf16, int sms,
+                             cudaStream_t stream);
 
 }  // namespace fa
