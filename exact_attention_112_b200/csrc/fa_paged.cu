@@ -52,7 +52,7 @@ constexpr int kPlanWarp = 10;
 // Register split (launch pool 168 x 384 = 64512 = 256 * 192 + 128 * 120).
 constexpr uint32_t kRegsSoftmax = 192;
 constexpr uint32_t kRegsOther = 120;
-constexpr int kDescs = 4;           // segment descriptors in the ring
+constexpr int kDescs = 8;           // segment descriptors in the ring
 constexpr float kTau = 8.0f;        // lazy-rescale threshold (log2 units)
 constexpr int kEmuEvery = 4;        // one pair of exponentials in kEmuEvery on the FMA pipe
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -255,6 +255,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
         }
         if (lane == 0) p.meta[blockIdx.x] = mm;
+        grid_launch_dependents();       // the merge may be set up; it waits for this grid
         named_bar_sync(1, kThreads);
     } else if (pc.b < 0) {
         named_bar_sync(1, kThreads);
@@ -277,19 +278,18 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const Seg s = descs[u % kDescs];
             desc_release(u);
             if (s.nt == 0) break;
-            // this lane's page and row of key tile kt (a page that is not to be
-            // read: one past the last, which TMA fills with zeros)
+            // this lane's table entry and row of key tile kt, asked for one tile
+            // ahead; a page that is not to be read is one past the last, which
+            // TMA fills with zeros
             const int *table = p.kv.table + s.b * p.kv.table_stride;
-            int page = 0, row = 0;
+            int entry = -1, row = 0;
             auto look_up = [&](int kt) {
                 const int key = kt * kBN + lane_box * p.box;
-                page = p.kv.num_pages;
-                row = 0;
+                entry = -1;
                 if (copies && key < s.len_k) {
                     const int pi = key / p.kv.page_size;
                     row = key - pi * p.kv.page_size;
-                    const int g = __ldg(table + pi);
-                    if (g >= 0 && g < p.kv.num_pages) page = g;
+                    entry = __ldg(table + pi);
                 }
             };
             look_up(s.t0);
@@ -307,7 +307,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int j = 0; j < s.nt && ok; ++j, ++t) {
                 const int st = t % kStages;
                 const uint32_t ph = (t / kStages) & 1;
-                const int pg = page, rw = row;
+                const int pg = entry >= 0 && entry < p.kv.num_pages ? entry : p.kv.num_pages, rw = row;
                 if (!mbar_wait_warp(bar(L::kKEmpty + st), ph ^ 1, wctx)) { ok = false; break; }
                 if (lane == 0) mbar_arrive_expect_tx(bar(L::kKFull + st), L::kTileBytes);
                 __syncwarp();
@@ -343,7 +343,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         constexpr uint32_t idesc_qk = idesc_f16_f32acc(BF16, kBM, kBN, false, false);
         constexpr uint32_t idesc_pv = idesc_f16_f32acc(BF16, kBM, D, false, true);
         struct Cursor {
-            int u = 0, j = 0, g = 0, t = 0;     // segment, its job, jobs and key tiles so far
+            int u = 0, j = 0, g = 0, t = 0;     // segment, its next job, jobs and key tiles so far
             int jobs = 0, two = 0, tail = kBN;
         };
         bool ok = true, any = false;
@@ -358,16 +358,8 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         };
         Cursor cs, cp;
         int q_n = 0;            // row tiles taken so far
-        // S of the next job: into the S columns of slot g & 1
-        auto step_s = [&]() -> bool {
-            if (cs.jobs == 0) return true;
-            const int slot = cs.g & 1, st = cs.t % kStages;
-            const int qi = cs.two ? (cs.j & 1) : 0;
-            const int bf = (q_n + qi) & 1;
-            if (cs.j <= cs.two && !mbar_wait_warp(bar(L::kQFull + bf), ((q_n + qi) >> 1) & 1, wctx)) return false;
-            if (!mbar_wait_warp(bar(L::kKFull + st), (cs.t / kStages) & 1, wctx)) return false;
-            tc_fence_after();
-            const bool tile_done = !cs.two || (cs.j & 1);
+        // S of a job, into the S columns of the slot
+        auto issue_s = [&](int slot, int bf, int st, bool k_done, bool q_done) {
             const uint64_t dq = smem_desc_sw128(sbase + L::kQ + bf * L::kTileBytes, 16, 1024);
             const uint64_t dk = smem_desc_sw128(sbase + L::kK + st * L::kTileBytes, 16, 1024);
             const uint32_t d = tmem + L::kColS + slot * 128;
@@ -378,10 +370,22 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     umma_f16_ss(d, dq + off, dk + off, idesc_qk, kk > 0);
                 }
                 umma_commit(bar(L::kSFull + slot));
-                if (tile_done) umma_commit(bar(L::kKEmpty + st));
-                if (cs.j + 1 + cs.two >= cs.jobs) umma_commit(bar(L::kQEmpty + bf));
+                if (k_done) umma_commit(bar(L::kKEmpty + st));
+                if (q_done) umma_commit(bar(L::kQEmpty + bf));
             }
             __syncwarp();
+        };
+        auto wait_k = [&](int t) { return mbar_wait_warp(bar(L::kKFull + t % kStages), (t / kStages) & 1, wctx); };
+        // the next job's S, whatever segment it is in
+        auto step_s = [&]() -> bool {
+            if (cs.jobs == 0) return true;
+            const int qi = cs.two ? (cs.j & 1) : 0;
+            const int bf = (q_n + qi) & 1;
+            const bool tile_done = !cs.two || (cs.j & 1);
+            if (cs.j <= cs.two && !mbar_wait_warp(bar(L::kQFull + bf), ((q_n + qi) >> 1) & 1, wctx)) return false;
+            if (!wait_k(cs.t)) return false;
+            tc_fence_after();
+            issue_s(cs.g & 1, bf, cs.t % kStages, tile_done, cs.j + 1 + cs.two >= cs.jobs);
             any = true;
             if (tile_done) ++cs.t;
             ++cs.g;
@@ -392,58 +396,96 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             return true;
         };
-        ok = enter(cs);
-        cp = cs;
-        for (int i = 0; i < 2 && ok; ++i) ok = step_s();
-        while (ok && cp.jobs > 0) {
-            // ---- P V of the oldest job, half by half
-            const int slot = cp.g & 1, st = cp.t % kStages;
-            const uint32_t pp = (cp.g >> 1) & 1;
-            if (!mbar_wait_warp(bar(L::kVFull + st), (cp.t / kStages) & 1, wctx)) { ok = false; break; }
-            if (cp.tail < kBN && cp.j >= cp.jobs - 1 - cp.two && (!cp.two || !(cp.j & 1))) {
-                // the sequence ends inside this key tile: P is 0 past it, but the
-                // cache may hold anything there (NaN), so V is made 0 too
-                const int n = (kBN - cp.tail) * 8;
-                for (int c = 0; c < L::kChunks; ++c) {
-                    uint4 *z = reinterpret_cast<uint4 *>(smem + L::kV + st * L::kTileBytes + c * L::kChunkBytes +
-                                                         cp.tail * 128);
-                    for (int e = lane; e < n; e += 32) z[e] = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
+        // P V of a job, half by half as the softmax hands P over
+        auto issue_pv = [&](int slot, uint32_t ph, int st, bool acc, bool v_done, bool o_done) -> bool {
             const uint64_t dv = smem_desc_sw128(sbase + L::kV + st * L::kTileBytes, L::kChunkBytes, 1024);
             const uint32_t pa = tmem + L::kColS + slot * 128;
             const uint32_t d = tmem + L::kColO + slot * D;
-            const bool acc = cp.j >= 2;
+#pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (!mbar_wait_warp(bar(L::kPHalf + 2 * slot + h), pp, wctx)) { ok = false; break; }
+                if (!mbar_wait_warp(bar(L::kPHalf + 2 * slot + h), ph, wctx)) return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_f16_ts(d, pa + (4 * h + kk) * 8, dv + ((static_cast<uint32_t>(4 * h + kk) * 16 * 128) >> 4),
                                     idesc_pv, acc || h + kk > 0);
+                    if (h == 1) {
+                        if (v_done) umma_commit(bar(L::kVEmpty + st));
+                        if (o_done) umma_commit(bar(L::kOFull + slot));
+                    }
                 }
                 __syncwarp();
             }
+            return true;
+        };
+        // V of key tile t; where the sequence ends inside it P is 0 past the end,
+        // but the cache may hold anything there (NaN), so V is made 0 too
+        auto wait_v = [&](int t, int valid) -> bool {
+            const int st = t % kStages;
+            if (!mbar_wait_warp(bar(L::kVFull + st), (t / kStages) & 1, wctx)) return false;
+            if (valid < kBN) {
+                for (int c = 0; c < L::kChunks; ++c) {
+                    uint4 *z = reinterpret_cast<uint4 *>(smem + L::kV + st * L::kTileBytes + c * L::kChunkBytes +
+                                                         valid * 128);
+                    for (int e = lane; e < (kBN - valid) * 8; e += 32) z[e] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            return true;
+        };
+        ok = enter(cs);
+        cp = cs;
+        for (int i = 0; i < 2 && ok; ++i) ok = step_s();
+        // PV(q), S(q + 2) for every job q; the S of the segment's own later
+        // tiles without step_s's bookkeeping (a wait that is not needed costs the
+        // MMA warp some 300 cycles of a 1700-cycle job)
+        while (ok && cp.jobs > 0) {
+            if (cp.two) {
+                const int nt = cp.jobs >> 1, sa = cp.g & 1, sb = sa ^ 1;
+                const int qa = (cs.u == cp.u ? q_n : 0) & 1, qb = qa ^ 1;     // used while S of this segment are left
+                for (int j = 0; j < nt; ++j) {
+                    const bool last = j + 1 == nt;
+                    const int st = cp.t % kStages, st1 = (cp.t + 1) % kStages;
+                    if (!(ok = wait_v(cp.t, last ? cp.tail : kBN))) break;
+                    if (!(ok = issue_pv(sa, (cp.g >> 1) & 1, st, j > 0, false, last))) break;
+                    if (!last) {
+                        if (!(ok = wait_k(cp.t + 1))) break;
+                        tc_fence_after();
+                        issue_s(sa, qa, st1, false, j + 2 == nt);
+                    } else if (!(ok = step_s())) {
+                        break;
+                    }
+                    if (!(ok = issue_pv(sb, ((cp.g + 1) >> 1) & 1, st, j > 0, true, last))) break;
+                    if (!last) {
+                        issue_s(sb, qb, st1, true, j + 2 == nt);
+                        if (j + 2 == nt) {
+                            cs.g = cp.g + 4;
+                            cs.t = cp.t + 2;
+                            q_n += 2;
+                            ++cs.u;
+                            if (!(ok = enter(cs))) break;
+                        }
+                    } else if (!(ok = step_s())) {
+                        break;
+                    }
+                    cp.g += 2;
+                    ++cp.t;
+                }
+            } else {
+                for (int j = 0; j < cp.jobs; ++j) {
+                    if (!(ok = wait_v(cp.t, j + 1 == cp.jobs ? cp.tail : kBN))) break;
+                    if (!(ok = issue_pv(cp.g & 1, (cp.g >> 1) & 1, cp.t % kStages, j >= 2, true, j + 2 >= cp.jobs))) break;
+                    if (!(ok = step_s())) break;
+                    ++cp.g;
+                    ++cp.t;
+                }
+            }
             if (!ok) break;
-            const bool tile_done = !cp.two || (cp.j & 1);
-            if (elect_one()) {
-                if (tile_done) umma_commit(bar(L::kVEmpty + st));
-                if (cp.j + 2 >= cp.jobs) umma_commit(bar(L::kOFull + slot));
-            }
-            __syncwarp();
-            if (tile_done) ++cp.t;
-            ++cp.g;
-            if (++cp.j == cp.jobs) {
-                desc_release(cp.u);
-                ++cp.u;
-                if (!step_s() || !enter(cp)) { ok = false; break; }
-            } else if (!step_s()) {
-                ok = false;
-                break;
-            }
+            desc_release(cp.u);
+            ++cp.u;
+            ok = enter(cp);
         }
         if (any) {
             // every issued MMA must finish before tensor memory is released
@@ -467,43 +509,41 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t tS = tl + L::kColS + slot * 128;
         const float qk = p.qk_scale_log2;
-        const int r_tok = row / p.G, r_head = row - r_tok * p.G;
         bool ok = true;
         int g0 = 0;                         // jobs before this segment
-        int o_n0 = 0, o_n1 = 0;             // segments that used slot 0 and 1
-        int merges = 0;
+        uint32_t ph = 0;                    // parities: bit s the O of slot s, bit 2 the merges
         for (int u = 0;; ++u) {
             if (!desc_wait(u)) break;
-            const Seg s = descs[u % kDescs];
-            desc_release(u);
+            const Seg &s = descs[u % kDescs];               // held until its results are written
             if (s.nt == 0) break;
             const int jobs = s.two ? 2 * s.nt : s.nt;
             const int first = (slot ^ g0) & 1;              // this slot's first job
-            const uint32_t o_ph[2] = {static_cast<uint32_t>(o_n0 & 1), static_cast<uint32_t>(o_n1 & 1)};
-            if (jobs > 1) {
-                ++o_n0;
-                ++o_n1;
-            } else if (g0 & 1) {
-                ++o_n1;
-            } else {
-                ++o_n0;
-            }
+            const uint32_t uses = jobs > 1 ? 3u : 1u << (g0 & 1);   // slots of this segment
             if (first >= jobs) {                            // a single job, the other slot's
                 g0 += jobs;
+                ph ^= uses;
+                desc_release(u);
                 continue;
             }
-            const int qt = s.two ? first : 0;               // row tile
-            const int tok = qt * p.geom.tile_tokens + r_tok;
-            const bool valid = r_tok < p.geom.tile_tokens && tok < s.ntok;
-            const bool active = __any_sync(0xffffffffu, valid);
-            const int lim = p.causal ? min(s.lim0 + tok, s.len_k - 1) : s.len_k - 1;
-            // rows of nothing keep a finite reference maximum; what they compute is not used
-            float m_ref = valid ? neg_inf() : 0.f;          // log2 units
+            bool active;                                    // the warp has rows
+            int lim;                                        // last key that the row sees
+            float m_ref;                                    // log2 units
+            {
+                const int tok = (s.two ? first * p.geom.tile_tokens : 0) + row / p.G;
+                const bool valid = row < p.geom.tile_tokens * p.G && tok < s.ntok;
+                active = __any_sync(0xffffffffu, valid);
+                lim = p.causal ? min(s.lim0 + tok, s.len_k - 1) : s.len_k - 1;
+                // rows of nothing: a reference maximum that no score exceeds, P = 0
+                m_ref = valid ? neg_inf() : 1e30f;
+            }
             float l = 0.f;
-            for (int j = first; j < jobs; j += 2) {
-                const int kv0 = (s.t0 + (s.two ? j >> 1 : j)) * kBN;
+            const int kv_step = s.two ? kBN : 2 * kBN;
+            int kv0 = (s.t0 + (s.two ? 0 : first)) * kBN;
+            uint32_t s_ph = ((g0 + first) >> 1) & 1;
+            bool later = false;                             // not the segment's first job here
+            for (int n = (jobs - first + 1) >> 1; n > 0; --n, kv0 += kv_step, s_ph ^= 1, later = true) {
                 {
-                    const bool got = mbar_wait(bar(L::kSFull + slot), ((g0 + j) >> 1) & 1, wctx);
+                    const bool got = mbar_wait(bar(L::kSFull + slot), s_ph, wctx);
                     if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 }
                 tc_fence_after();
@@ -533,7 +573,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 const float m_tile =
                     qk * fmax3(fmax3(mx0, mx1, x[124]), fmax3(mx2, mx3, x[125]), fmaxf(x[126], x[127]));
-                const bool need = valid && m_tile > m_ref + kTau;
+                const bool need = m_tile > m_ref + kTau;
                 const bool rescale = __any_sync(0xffffffffu, need);     // warp-uniform
                 float alpha = 1.f;
                 if (rescale) {
@@ -575,7 +615,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     half(0, std::true_type{});
                 else
                     half(0, std::false_type{});
-                if (rescale && j > 1) {
+                if (rescale && later) {
                     // O row *= alpha.  O is stable: this S tile's MMA was issued
                     // after the slot's previous P V and its commit covers it.
                     const uint32_t tO = tl + L::kColO + slot * D;
@@ -603,6 +643,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
 
             // ---- the rows' results: O = o / l, LSE = (m_ref + log2 l) ln 2
+            const int r_tok = row / p.G, r_head = row - r_tok * p.G;
+            const int tok = (s.two ? first * p.geom.tile_tokens : 0) + r_tok;
+            const bool valid = r_tok < p.geom.tile_tokens && tok < s.ntok;
             const int ur = tok * p.G + r_head;              // row of the unit
             const int t = s.row0 + tok, head = s.h * p.G + r_head;
             uint16_t *o_row = nullptr;
@@ -642,7 +685,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     p.lse_part[(2 * blockIdx.x + s.dest) * static_cast<size_t>(p.part_rows) + ur] = lse2;
             };
             if (s.two || jobs == 1) {
-                const bool got = mbar_wait(bar(L::kOFull + slot), o_ph[slot], wctx);
+                const bool got = mbar_wait(bar(L::kOFull + slot), (ph >> slot) & 1, wctx);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 tc_fence_after();
                 if (active) {
@@ -664,8 +707,8 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 // the same rows; each warpgroup adds up half of the columns
                 stats[slot * kBM + row] = make_float2(m_ref, l);
                 mbar_arrive(bar(L::kStat));
-                bool got = mbar_wait(bar(L::kStat), merges & 1, wctx) && mbar_wait(bar(L::kOFull + 0), o_ph[0], wctx) &&
-                           mbar_wait(bar(L::kOFull + 1), o_ph[1], wctx);
+                bool got = mbar_wait(bar(L::kStat), (ph >> 2) & 1, wctx) && mbar_wait(bar(L::kOFull + 0), ph & 1, wctx) &&
+                           mbar_wait(bar(L::kOFull + 1), (ph >> 1) & 1, wctx);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 tc_fence_after();
                 if (active) {
@@ -693,11 +736,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 // both read the other's O and statistics before either is replaced
                 tc_fence_before();
                 mbar_arrive(bar(L::kRead));
-                got = mbar_wait(bar(L::kRead), merges & 1, wctx);
+                got = mbar_wait(bar(L::kRead), (ph >> 2) & 1, wctx);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                ++merges;
+                ph ^= 4;
             }
+            ph ^= uses;
             g0 += jobs;
+            desc_release(u);
         }
         __syncwarp();
         named_bar_sync(1, kThreads);
@@ -714,6 +759,7 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
     constexpr int kPer = D / 32;
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int ur = blockIdx.y * 8 + (threadIdx.x >> 5);
+    grid_dependency_wait();             // the partial results are complete and visible
     const MergeMeta mm = p.meta[c];
     if (mm.last < 0 || ur >= mm.tokens * p.G) return;
     auto index = [&](int i) -> size_t {
@@ -765,10 +811,19 @@ cudaError_t launch_t(const PagedTensorMaps &tm, const PagedFwdParams &p, int gri
     note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     prof_begin(stream, "fa_paged_merge_kernel");
-    fa_paged_merge_kernel<D, BF16><<<dim3(grid, (p.part_rows + 7) / 8), 256, 0, stream>>>(p);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, (p.part_rows + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, BF16>, p);
     prof_end(stream);
     note_launch();
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
