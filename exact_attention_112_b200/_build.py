@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
-SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_paged_api.cu", "fa_rope.cu", "fa_paged.cu"]
+SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_paged_api.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_tokens.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -57,18 +57,6 @@ constexpr float kTau = 8.0f;        // lazy-rescale threshold (log2 units)
 constexpr int kEmuEvery = 4;        // one pair of exponentials in kEmuEvery on the FMA pipe
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// A segment: key tiles [t0, t0 + nt) of a unit (nt == 0: the end of the work).
-struct Seg {
-    int row0, ntok;     // first row of the packed tensors, tokens
-    int h, b;           // kv head, sequence
-    int len_k, lim0;    // keys of the sequence; last key the first token sees
-    int t0, nt;
-    int two;            // two tiles of query rows
-    int tail;           // keys below len_k in the last key tile
-    int dest;           // -1: the rows' results, else partial result `dest` of this CTA
-    int pad;
-};
-
 template <int D>
 struct PagedLayout {
     static constexpr int kStages = D == 64 ? 4 : 2;       // K and V tiles in flight each
@@ -105,35 +93,10 @@ struct PagedLayout {
     static_assert(sizeof(Seg) % 16 == 0, "descriptors are copied as int4");
 };
 
-__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if constexpr (BF16) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<uint32_t *>(&h);
-    } else {
-        __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<uint32_t *>(&h);
-    }
-}
-
 __device__ __forceinline__ void st_global_v8(void *p, const uint32_t *a) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a[0]), "r"(a[1]),
                  "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])
                  : "memory");
-}
-
-// Rows without a visible key: O = 0, LSE = -inf.
-template <int D>
-__device__ __forceinline__ void write_empty(const PagedFwdParams &p, int row0, int ntok, int h, int lane) {
-    const int n = ntok * p.G;
-    for (int r = lane; r < n; r += 32) {
-        const int t = row0 + r / p.G, head = h * p.G + r % p.G;
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + head * p.o_h + t * p.o_n);
-        for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
-        p.lse[static_cast<long long>(head) * p.T + t] = neg_inf();
-    }
 }
 
 template <int D, bool BF16>
@@ -141,9 +104,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedFwdParams p) {
     using L = PagedLayout<D>;
+    using KT = KeyTile<D>;
     constexpr int kStages = L::kStages;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ PlanSmem plan_smem;
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -156,6 +119,8 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
+    PlanSeqs seqs;
+    if (warp == kPlanWarp) plan_load(p, lane, seqs);    // the tables arrive during the set-up
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
         tmem_relinquish();
@@ -190,7 +155,6 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    const Piece pc = plan_piece<kThreads>(p, p.geom, p.min_piece, plan_smem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -212,7 +176,8 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (warp == kPlanWarp) {
         // ===================== the CTA's share of the work =====================
         MergeMeta mm{0, 0, 0, -1};
-        if (pc.b >= 0) {
+        {
+            const Piece pc = plan_piece(p, p.geom, p.min_piece, lane, seqs);
             bool ok = true;
             int u = 0;
             auto push = [&](const Seg &s) -> bool {
@@ -225,50 +190,28 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 ++u;
                 return true;
             };
-            SegWalk w;
-            w.first(p, p.geom, pc);
-            do {
-                const int ntok = min(p.geom.unit_tokens, w.s.new_q - w.tok0), row0 = w.s.q0 + w.tok0;
-                if (w.n == 0) {
-                    write_empty<D>(p, row0, ntok, w.h, lane);
-                } else if (!w.none()) {
-                    Seg s;
-                    s.row0 = row0;
-                    s.ntok = ntok;
-                    s.h = w.h;
-                    s.b = w.b;
-                    s.len_k = w.s.len_k;
-                    s.lim0 = w.tok0 + w.s.len_k - w.s.new_q;
-                    s.t0 = w.t0;
-                    s.nt = w.t1 - w.t0;
-                    s.two = w.two;
-                    s.tail = min(kBN, w.s.len_k - (w.t1 - 1) * kBN);
-                    s.dest = w.whole() ? -1 : (w.t0 == 0 ? 1 : 0);
-                    s.pad = 0;
-                    if (w.t0 == 0 && w.t1 < w.n) mm = MergeMeta{row0, ntok, w.h, w.last_cta(pc)};
-                    ok = push(s);
-                }
-            } while (ok && w.next(p, p.geom));
-            if (ok) {
-                Seg s{};
-                push(s);
+            if (pc.b >= 0) {
+                SegWalk w;
+                w.first(p, p.geom, pc);
+                do {
+                    const Seg s = make_seg(w, p.geom);
+                    if (w.n == 0) {
+                        write_empty<D>(p, s.row0, s.ntok, s.h, lane);
+                    } else if (!w.none()) {
+                        if (w.t0 == 0 && w.t1 < w.n) mm = MergeMeta{s.row0, s.ntok, s.h, w.last_cta(pc)};
+                        ok = push(s);
+                    }
+                } while (ok && w.next(p, p.geom));
             }
+            if (ok) push(Seg{});
         }
         if (lane == 0) p.meta[blockIdx.x] = mm;
         grid_launch_dependents();       // the merge may be set up; it waits for this grid
         named_bar_sync(1, kThreads);
-    } else if (pc.b < 0) {
-        named_bar_sync(1, kThreads);
-        if (warp == kMmaWarp) {
-            __syncwarp();
-            tmem_dealloc(tmem, L::kTmemCols);
-        }
     } else if (warp == kProducerWarp) {
         // ===================== TMA producer =====================
-        const int boxes = kBN / p.box;
-        const int lane_box = lane / L::kChunks, lane_chunk = lane % L::kChunks;
-        const bool copies = lane_box < boxes;
-        const uint32_t dst = lane_chunk * L::kChunkBytes + lane_box * p.box * 128;
+        PageBoxes pages;
+        pages.init(p, lane);
         const uint32_t q_bytes = static_cast<uint32_t>(L::kChunks * 128 * p.G * p.geom.tile_tokens);
         int t = 0;          // key tiles begun so far (ring position)
         int k_n = 0, v_n = 0, q_n = 0;      // copies issued
@@ -278,21 +221,8 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const Seg s = descs[u % kDescs];
             desc_release(u);
             if (s.nt == 0) break;
-            // this lane's table entry and row of key tile kt, asked for one tile
-            // ahead; a page that is not to be read is one past the last, which
-            // TMA fills with zeros
-            const int *table = p.kv.table + s.b * p.kv.table_stride;
-            int entry = -1, row = 0;
-            auto look_up = [&](int kt) {
-                const int key = kt * kBN + lane_box * p.box;
-                entry = -1;
-                if (copies && key < s.len_k) {
-                    const int pi = key / p.kv.page_size;
-                    row = key - pi * p.kv.page_size;
-                    entry = __ldg(table + pi);
-                }
-            };
-            look_up(s.t0);
+            pages.segment(p, s);
+            pages.look_up(p, s.t0, s.len_k);
             for (int i = 0; i <= s.two && ok; ++i, ++q_n) {
                 const int bf = q_n & 1;
                 if (!mbar_wait_warp(bar(L::kQEmpty + bf), ((q_n >> 1) & 1) ^ 1, wctx)) { ok = false; break; }
@@ -307,21 +237,17 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int j = 0; j < s.nt && ok; ++j, ++t) {
                 const int st = t % kStages;
                 const uint32_t ph = (t / kStages) & 1;
-                const int pg = entry >= 0 && entry < p.kv.num_pages ? entry : p.kv.num_pages, rw = row;
+                const PageBoxes::Box kb = pages.box(p, p.k_ratio), vb = pages.box(p, p.v_ratio);
                 if (!mbar_wait_warp(bar(L::kKEmpty + st), ph ^ 1, wctx)) { ok = false; break; }
                 if (lane == 0) mbar_arrive_expect_tx(bar(L::kKFull + st), L::kTileBytes);
                 __syncwarp();
-                if (copies)
-                    tma_load_4d(sbase + L::kK + st * L::kTileBytes + dst, &tm_k, bar(L::kKFull + st), lane_chunk * 64,
-                                rw, s.h, pg);
+                pages.copy(p, &tm_k, sbase + L::kK + st * L::kTileBytes, KT::kGroupBytes, bar(L::kKFull + st), kb);
                 ++k_n;
-                if (j + 1 < s.nt) look_up(s.t0 + j + 1);
+                if (j + 1 < s.nt) pages.look_up(p, s.t0 + j + 1, s.len_k);
                 if (!mbar_wait_warp(bar(L::kVEmpty + st), ph ^ 1, wctx)) { ok = false; break; }
                 if (lane == 0) mbar_arrive_expect_tx(bar(L::kVFull + st), L::kTileBytes);
                 __syncwarp();
-                if (copies)
-                    tma_load_4d(sbase + L::kV + st * L::kTileBytes + dst, &tm_v, bar(L::kVFull + st), lane_chunk * 64,
-                                rw, s.h, pg);
+                pages.copy(p, &tm_v, sbase + L::kV + st * L::kTileBytes, KT::kGroupBytes, bar(L::kVFull + st), vb);
                 ++v_n;
             }
         }
@@ -361,13 +287,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         // S of a job, into the S columns of the slot
         auto issue_s = [&](int slot, int bf, int st, bool k_done, bool q_done) {
             const uint64_t dq = smem_desc_sw128(sbase + L::kQ + bf * L::kTileBytes, 16, 1024);
-            const uint64_t dk = smem_desc_sw128(sbase + L::kK + st * L::kTileBytes, 16, 1024);
+            const uint64_t dk = KT::k_desc(sbase + L::kK + st * L::kTileBytes);
             const uint32_t d = tmem + L::kColS + slot * 128;
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
-                    umma_f16_ss(d, dq + off, dk + off, idesc_qk, kk > 0);
+                    umma_f16_ss(d, dq + off, dk + KT::k_step(kk), idesc_qk, kk > 0);
                 }
                 umma_commit(bar(L::kSFull + slot));
                 if (k_done) umma_commit(bar(L::kKEmpty + st));
@@ -398,7 +324,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         };
         // P V of a job, half by half as the softmax hands P over
         auto issue_pv = [&](int slot, uint32_t ph, int st, bool acc, bool v_done, bool o_done) -> bool {
-            const uint64_t dv = smem_desc_sw128(sbase + L::kV + st * L::kTileBytes, L::kChunkBytes, 1024);
+            const uint64_t dv = KT::v_desc(sbase + L::kV + st * L::kTileBytes, true);
             const uint32_t pa = tmem + L::kColS + slot * 128;
             const uint32_t d = tmem + L::kColO + slot * D;
 #pragma unroll
@@ -408,8 +334,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_f16_ts(d, pa + (4 * h + kk) * 8, dv + ((static_cast<uint32_t>(4 * h + kk) * 16 * 128) >> 4),
-                                    idesc_pv, acc || h + kk > 0);
+                        umma_f16_ts(d, pa + (4 * h + kk) * 8, dv + KT::v_step(4 * h + kk), idesc_pv, acc || h + kk > 0);
                     if (h == 1) {
                         if (v_done) umma_commit(bar(L::kVEmpty + st));
                         if (o_done) umma_commit(bar(L::kOFull + slot));
@@ -425,11 +350,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const int st = t % kStages;
             if (!mbar_wait_warp(bar(L::kVFull + st), (t / kStages) & 1, wctx)) return false;
             if (valid < kBN) {
-                for (int c = 0; c < L::kChunks; ++c) {
-                    uint4 *z = reinterpret_cast<uint4 *>(smem + L::kV + st * L::kTileBytes + c * L::kChunkBytes +
-                                                         valid * 128);
-                    for (int e = lane; e < (kBN - valid) * 8; e += 32) z[e] = make_uint4(0, 0, 0, 0);
-                }
+                KT::clear(smem + L::kV + st * L::kTileBytes, valid, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
             }
@@ -810,7 +731,11 @@ cudaError_t launch_t(const PagedTensorMaps &tm, const PagedFwdParams &p, int gri
     prof_end(stream);
     note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    prof_begin(stream, "fa_paged_merge_kernel");
+    return launch_paged_merge(p, BF16, grid, stream);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_merge_t(const PagedFwdParams &p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid, (p.part_rows + 7) / 8);
     cfg.blockDim = dim3(256);
@@ -820,7 +745,8 @@ cudaError_t launch_t(const PagedTensorMaps &tm, const PagedFwdParams &p, int gri
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, BF16>, p);
+    prof_begin(stream, "fa_paged_merge_kernel");
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, BF16>, p);
     prof_end(stream);
     note_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -833,6 +759,11 @@ cudaError_t launch_paged_fwd(const PagedTensorMaps &tm, const PagedFwdParams &p,
     const int grid = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
     if (p.kv.D == 64) return bf16 ? launch_t<64, true>(tm, p, grid, stream) : launch_t<64, false>(tm, p, grid, stream);
     return bf16 ? launch_t<128, true>(tm, p, grid, stream) : launch_t<128, false>(tm, p, grid, stream);
+}
+
+cudaError_t launch_paged_merge(const PagedFwdParams &p, bool bf16, int grid, cudaStream_t stream) {
+    if (p.kv.D == 64) return bf16 ? launch_merge_t<64, true>(p, grid, stream) : launch_merge_t<64, false>(p, grid, stream);
+    return bf16 ? launch_merge_t<128, true>(p, grid, stream) : launch_merge_t<128, false>(p, grid, stream);
 }
 
 }  // namespace fa

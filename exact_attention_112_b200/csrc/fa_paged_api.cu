@@ -133,6 +133,10 @@ fa::SchedGeom sched_geom(int G, int max_q) {
     g.tile = 128;
     g.tile_tokens = std::max(1, std::min(128 / G, max_q));
     g.unit_tokens = std::max(1, std::min(2 * (128 / G), max_q));
+    if (max_q * G <= fa::kPagedTokenRows) g.tile_tokens = g.unit_tokens;    // one unit per sequence and kv head
+    // a key tile of one row tile takes 1.44 us, of two 2.03
+    g.one_cost = g.unit_tokens > g.tile_tokens ? 5 : 1;
+    g.two_cost = 7;
     return g;
 }
 
@@ -147,6 +151,30 @@ PagedWorkspace paged_workspace(const fa::SchedGeom &g, int G, int D) {
     w.meta = w.lse + (rows * sizeof(float) + 15) / 16 * 16;
     w.bytes = w.meta + fa::kPagedMaxCtas * sizeof(fa::MergeMeta);
     return w;
+}
+
+// Pages and heads as one dimension: index page * ratio + head, `extent` entries
+// (0: not possible) `stride` elements apart.
+struct PageFold {
+    int ratio;
+    long long extent, stride;
+};
+
+PageFold page_fold(const fa::PagedCache &c, long long page, long long head) {
+    PageFold f{1, 0, 0};
+    if (c.Hkv == 1) {
+        f.stride = page;
+    } else if (c.num_pages == 1 || page % head == 0) {
+        const long long r = c.num_pages == 1 ? 0 : page / head;
+        if (r > INT32_MAX) return f;
+        f.ratio = static_cast<int>(r);
+        f.stride = head;
+    } else {
+        return f;
+    }
+    const long long n = static_cast<long long>(c.num_pages - 1) * f.ratio + c.Hkv;
+    if (n <= INT32_MAX) f.extent = n;
+    return f;
 }
 
 int encode(CUtensorMap *m, const void *ptr, bool bf16, int rank, const cuuint64_t *dims, const long long *strides,
@@ -267,11 +295,12 @@ int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_stride
     p.causal = causal;
     p.qk_scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
     p.geom = sched_geom(G, p.max_q);
-    // a CTA takes two key tiles at least (it works on two at a time)
-    p.min_piece = p.geom.unit_tokens > p.geom.tile_tokens ? 4 : 2;
-    p.box = std::gcd(kv->page_size, 128);
-    p.o_v8 = aligned(o, 32) && p.o_h % 16 == 0 && p.o_n % 16 == 0;
     p.part_rows = p.geom.unit_tokens * G;
+    const bool tokens = p.part_rows <= fa::kPagedTokenRows;
+    // the tile kernel works on two key tiles at a time; every piece holds the
+    // first entry of a key tile (two_cost <= min_piece / 2)
+    p.min_piece = tokens ? 1 : p.geom.one_cost > 1 ? 14 : 2;
+    p.o_v8 = aligned(o, 32) && p.o_h % 16 == 0 && p.o_n % 16 == 0;
     const PagedWorkspace w = paged_workspace(p.geom, G, D);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.o_part = reinterpret_cast<float *>(ws);
@@ -288,16 +317,39 @@ int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_stride
         const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(p.geom.tile_tokens)};
         if ((st = encode(&tm.q, q, bf16, 3, dims, str, box)) != FA_OK) return st;
     }
+    // The caches as [.., 8 rows, D / 64, 64]: a box is a run of a page's rows, one
+    // head.  With five dimensions there is room for the groups of eight rows or for
+    // the head; pages and heads become one dimension where the page stride is a
+    // multiple of the head stride (any cache without odd padding), else a box is
+    // eight rows.
+    const PageFold kf = page_fold(p.kv, p.kv.k_page, p.kv.k_head), vf = page_fold(p.kv, p.kv.v_page, p.kv.v_head);
+    p.fold = kf.extent > 0 && vf.extent > 0;
+    p.box = p.fold ? std::gcd(kv->page_size, 128) : 8;
+    p.k_ratio = kf.ratio;
+    p.v_ratio = vf.ratio;
     for (int i = 0; i < 2; ++i) {
-        const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(kv->page_size),
-                                    static_cast<cuuint64_t>(kv->num_kv_heads), static_cast<cuuint64_t>(kv->num_pages)};
-        const long long str[3] = {i ? p.kv.v_tok : p.kv.k_tok, i ? p.kv.v_head : p.kv.k_head,
-                                  i ? p.kv.v_page : p.kv.k_page};
-        const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.box), 1, 1};
-        if ((st = encode(i ? &tm.v : &tm.k, i ? p.kv.v : p.kv.k, bf16, 4, dims, str, box)) != FA_OK) return st;
+        const long long tok = i ? p.kv.v_tok : p.kv.k_tok, head = i ? p.kv.v_head : p.kv.k_head;
+        const PageFold &f = i ? vf : kf;
+        cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(D / 64)};
+        long long str[4] = {tok, 64};
+        cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), 1, 1};
+        if (p.fold) {
+            dims[3] = kv->page_size / 8;
+            str[2] = 8 * tok;
+            box[3] = p.box / 8;
+            dims[4] = f.extent;
+            str[3] = f.stride;
+        } else {
+            dims[1] = kv->page_size;
+            dims[3] = kv->num_kv_heads;
+            str[2] = head;
+            dims[4] = kv->num_pages;
+            str[3] = i ? p.kv.v_page : p.kv.k_page;
+        }
+        if ((st = encode(i ? &tm.v : &tm.k, i ? p.kv.v : p.kv.k, bf16, 5, dims, str, box)) != FA_OK) return st;
     }
-    return fa::launch_paged_fwd(tm, p, bf16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? FA_OK : FA_ERR_CUDA;
+    const auto launch = tokens ? fa::launch_paged_tokens : fa::launch_paged_fwd;
+    return launch(tm, p, bf16, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

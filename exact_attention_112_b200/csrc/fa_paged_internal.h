@@ -86,7 +86,8 @@ __host__ __device__ inline PagedSeq paged_seq(int b, const int *cu, const int *s
 struct SchedGeom {
     int tile;           // keys per tile
     int unit_tokens;    // tokens per unit
-    int tile_tokens;    // tokens per tile of query rows (a unit past it counts double)
+    int tile_tokens;    // tokens per tile of query rows (a unit past it has two)
+    int one_cost, two_cost;     // entries that a key tile of a unit of one or two row tiles counts
 };
 
 // What the merge kernel reads of CTA c: the unit that c begins and does not
@@ -108,7 +109,9 @@ struct PagedFwdParams {
     float qk_scale_log2;
     SchedGeom geom;
     int min_piece;                      // least entries worth a CTA
-    int box;                            // keys per TMA box: gcd(page_size, 128)
+    int box;                            // keys per TMA box: gcd(page_size, 128), 8 without fold
+    int fold;                           // pages and heads are one dimension of the tensor maps
+    int k_ratio, v_ratio;               // index (page, head) of that dimension: page * ratio + head
     int o_v8;                           // rows of o start 32-byte aligned
     int part_rows;                      // rows of a partial result: unit_tokens * G
     float *o_part;                      // [2 * kPagedMaxCtas, part_rows, D]
@@ -122,7 +125,15 @@ struct PagedTensorMaps {
     CUtensorMap q, k, v;
 };
 
+// Tiles of 128 query rows.
 cudaError_t launch_paged_fwd(const PagedTensorMaps &tm, const PagedFwdParams &p, bool bf16, int sms,
                              cudaStream_t stream);
+// All new tokens of a sequence in one unit of at most kPagedTokenRows query
+// rows (geom.unit_tokens * G).
+constexpr int kPagedTokenRows = 64;
+cudaError_t launch_paged_tokens(const PagedTensorMaps &tm, const PagedFwdParams &p, bool bf16, int sms,
+                                cudaStream_t stream);
+// Joins the partial results, after either.
+cudaError_t launch_paged_merge(const PagedFwdParams &p, bool bf16, int grid, cudaStream_t stream);
 
 }  // namespace fa

@@ -12,12 +12,16 @@
 // which a second kernel merges in the order of the CTAs, so the result does not
 // depend on timing.
 //
-// An entry is one key tile of a unit with one tile of query rows, a unit with
-// two counts each key tile twice.  A unit without a visible key counts as one
-// entry: its rows have to be written.
+// A key tile of a unit counts `one_cost` entries, or `two_cost` where the unit
+// has two tiles of query rows: about what the two take.  A unit without a
+// visible key counts as one tile: its rows have to be written.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include "fa_paged_internal.h"
+#include "fa_ptx.cuh"
 
 namespace fa {
 
@@ -32,8 +36,8 @@ __device__ __forceinline__ int unit_tiles(const PagedSeq &s, int tok0, const Sch
 }
 
 __device__ __forceinline__ long long unit_cost(const PagedSeq &s, int tok0, const SchedGeom &g, int causal) {
-    const int n = max(1, unit_tiles(s, tok0, g, causal));
-    return tok0 + g.tile_tokens < s.new_q ? 2ll * n : n;
+    const long long n = max(1, unit_tiles(s, tok0, g, causal));
+    return n * (tok0 + g.tile_tokens < s.new_q ? g.two_cost : g.one_cost);
 }
 
 // Work of one kv head of a sequence.
@@ -47,81 +51,94 @@ __device__ __forceinline__ PagedSeq load_seq(const PagedFwdParams &p, int b) {
     return paged_seq(b, p.cu, p.kv.seq_lens, p.T, p.max_q, static_cast<long long>(p.kv.max_pages) * p.kv.page_size);
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where they suffice (a 64-bit quotient is
+// a hundred dependent instructions, several of them a microsecond).
+__device__ __forceinline__ long long div_wide(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // One CTA's piece of the line, and where its first unit starts.
 struct Piece {
     long long lo, hi;       // entries [lo, hi)
     long long total;        // W
     int ctas;               // C
+    long long quot;         // W / C
+    int rem;                // W % C: the first `rem` pieces have one more
     long long start;        // first entry of sequence b
     int b;                  // sequence that holds entry lo (-1: no work)
+    PagedSeq s;             // its rows and keys
 };
 
-// Shared memory of plan_piece().
-struct PlanSmem {
-    long long warp_sum[32];
-    long long start;
-    int b;
+// The CTA's piece, computed by one warp (every lane gets the same).  A lane takes
+// every 32nd sequence; the first kPlanRounds of them stay in registers between
+// the sum and the search, so that a batch of up to 256 sequences costs one
+// latency of the tables.  min_piece: the least entries worth a CTA of its own.
+constexpr int kPlanRounds = 8;
+
+struct PlanSeqs {
+    PagedSeq s[kPlanRounds];
 };
 
-// Computed by all NT threads of the CTA together; the result is the same for
-// every thread.  min_piece: the least entries worth a CTA of its own.
-template <int NT>
-__device__ __forceinline__ Piece plan_piece(const PagedFwdParams &p, const SchedGeom &g, int min_piece, PlanSmem &sm) {
-    constexpr int kWarps = NT / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// The tables' part, to be asked for ahead of other set-up.
+__device__ __forceinline__ void plan_load(const PagedFwdParams &p, int lane, PlanSeqs &q) {
+#pragma unroll
+    for (int i = 0; i < kPlanRounds; ++i)
+        q.s[i] = 32 * i + lane < p.kv.num_seqs ? load_seq(p, 32 * i + lane) : PagedSeq{0, 0, 0};
+}
+
+__device__ __forceinline__ Piece plan_piece(const PagedFwdParams &p, const SchedGeom &g, int min_piece, int lane,
+                                            const PlanSeqs &q) {
     const int B = p.kv.num_seqs;
-    if (tid == 0) sm.b = -1;
+    auto cost = [&](const PagedSeq &s) { return p.kv.Hkv * head_cost(s, g, p.causal); };
     Piece pc;
-    pc.total = 0;
-    long long mine = 0;         // work of sequence tid of the (last) round of NT sequences
-    for (int b0 = 0; b0 < B; b0 += NT) {
-        mine = b0 + tid < B ? p.kv.Hkv * head_cost(load_seq(p, b0 + tid), g, p.causal) : 0;
-        pc.total += mine;
+    long long mine[kPlanRounds], v = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanRounds; ++i) {
+        mine[i] = 32 * i < B ? cost(q.s[i]) : 0;
+        v += mine[i];
     }
-    long long v = pc.total;
+    for (int b = 32 * kPlanRounds + lane; b < B; b += 32) v += cost(load_seq(p, b));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) sm.warp_sum[warp] = v;
-    __syncthreads();
-    pc.total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) pc.total += sm.warp_sum[w];
-    const long long most = (pc.total + min_piece - 1) / min_piece;
-    pc.ctas = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+    pc.total = v;
+    pc.ctas = pc.total >= static_cast<long long>(min_piece) * gridDim.x
+                  ? static_cast<int>(gridDim.x) : static_cast<int>(div_wide(pc.total + min_piece - 1, min_piece));
+    pc.quot = pc.ctas > 0 ? div_wide(pc.total, pc.ctas) : 0;
+    pc.rem = static_cast<int>(pc.total - pc.quot * pc.ctas);
     const int c = blockIdx.x;
-    if (c >= pc.ctas) {
-        pc.b = -1;
-        pc.lo = pc.hi = pc.start = 0;
-        return pc;              // the same branch for every thread
-    }
-    pc.lo = c * pc.total / pc.ctas;
-    pc.hi = (c + 1) * pc.total / pc.ctas;
-    long long base = 0;
-    for (int b0 = 0; b0 < B; b0 += NT) {
-        if (B > NT) mine = b0 + tid < B ? p.kv.Hkv * head_cost(load_seq(p, b0 + tid), g, p.causal) : 0;
-        long long inc = mine;
+    pc.b = -1;
+    pc.lo = pc.hi = pc.start = 0;
+    if (c >= pc.ctas) return pc;
+    pc.lo = c * pc.quot + min(c, pc.rem);
+    pc.hi = pc.lo + pc.quot + (c < pc.rem ? 1 : 0);
+    long long base = 0;     // entries before the round's sequences
+    auto round = [&](int b0, long long mine_b, const PagedSeq &s) {
+        long long inc = mine_b;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long x = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += x;
         }
-        __syncthreads();        // the sums of the round before have been read
-        if (lane == 31) sm.warp_sum[warp] = inc;
-        __syncthreads();
-        long long before = base;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += sm.warp_sum[w];
-            base += sm.warp_sum[w];
-        }
-        const long long at = before + inc - mine;
-        if (mine > 0 && at <= pc.lo && pc.lo < at + mine) {
-            sm.start = at;
-            sm.b = b0 + tid;
-        }
+        const long long at = base + inc - mine_b;
+        const unsigned hit = __ballot_sync(0xffffffffu, mine_b > 0 && at <= pc.lo && pc.lo < at + mine_b);
+        base += __shfl_sync(0xffffffffu, inc, 31);
+        if (hit == 0) return false;
+        const int l = __ffs(hit) - 1;
+        pc.b = b0 + l;
+        pc.start = __shfl_sync(0xffffffffu, at, l);
+        pc.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+        pc.s.new_q = __shfl_sync(0xffffffffu, s.new_q, l);
+        pc.s.len_k = __shfl_sync(0xffffffffu, s.len_k, l);
+        return true;
+    };
+#pragma unroll
+    for (int i = 0; i < kPlanRounds; ++i)
+        if (32 * i < B && round(32 * i, mine[i], q.s[i])) return pc;
+    for (int b0 = 32 * kPlanRounds; b0 < B; b0 += 32) {
+        const PagedSeq s = b0 + lane < B ? load_seq(p, b0 + lane) : PagedSeq{0, 0, 0};
+        if (round(b0, cost(s), s)) return pc;
     }
-    __syncthreads();
-    pc.b = sm.b;
-    pc.start = sm.start;
     return pc;
 }
 
@@ -133,6 +150,7 @@ struct SegWalk {
     int n;                  // key tiles of the unit
     int t0, t1;             // those of this segment
     bool two;               // two tiles of query rows
+    int w;                  // entries of a key tile
     long long base;         // the unit's first entry
     long long cost;
     // the piece
@@ -141,7 +159,8 @@ struct SegWalk {
     __device__ __forceinline__ void unit(const PagedFwdParams &p, const SchedGeom &g) {
         n = unit_tiles(s, tok0, g, p.causal);
         two = tok0 + g.tile_tokens < s.new_q;
-        cost = two ? 2ll * max(1, n) : max(1, n);
+        w = two ? g.two_cost : g.one_cost;
+        cost = static_cast<long long>(w) * max(1, n);
     }
 
     __device__ __forceinline__ void first(const PagedFwdParams &p, const SchedGeom &g, const Piece &pc) {
@@ -151,9 +170,9 @@ struct SegWalk {
         h = 0;
         tok0 = 0;
         base = pc.start;
-        s = load_seq(p, b);
+        s = pc.s;
         const long long per_head = head_cost(s, g, p.causal);
-        h = static_cast<int>((lo - base) / per_head);
+        h = static_cast<int>(div_wide(lo - base, per_head));
         base += h * per_head;
         unit(p, g);
         while (base + cost <= lo) {
@@ -164,11 +183,11 @@ struct SegWalk {
         range();
     }
 
+    // Key tile j is the CTA's that holds the unit's entry w * j.
     __device__ __forceinline__ void range() {
-        const int w = two ? 2 : 1;
         const long long a = lo - base, z = hi - base;
-        t0 = a <= 0 ? 0 : static_cast<int>(min(static_cast<long long>(n), (a + w - 1) / w));
-        t1 = static_cast<int>(min(static_cast<long long>(n), (z + w - 1) / w));
+        t0 = a <= 0 ? 0 : static_cast<int>(min(static_cast<long long>(n), div_wide(a + w - 1, w)));
+        t1 = z >= cost ? n : static_cast<int>(min(static_cast<long long>(n), div_wide(z + w - 1, w)));
     }
 
     // The next unit of the piece; false when there is none.
@@ -199,9 +218,136 @@ struct SegWalk {
 
     // CTA that holds the unit's last key tile.
     __device__ __forceinline__ int last_cta(const Piece &pc) const {
-        const long long at = base + (two ? 2ll : 1ll) * (n - 1);
-        return static_cast<int>(((at + 1) * pc.ctas - 1) / pc.total);
+        const long long at = base + static_cast<long long>(w) * (n - 1), wide = pc.rem * (pc.quot + 1);
+        return static_cast<int>(at < wide ? div_wide(at, pc.quot + 1) : pc.rem + div_wide(at - wide, pc.quot));
     }
 };
+
+// A segment as the kernels' roles hand it on: key tiles [t0, t0 + nt) of a unit
+// (nt == 0: the end of the work).
+struct Seg {
+    int row0, ntok;     // first row of the packed tensors, tokens
+    int h, b;           // kv head, sequence
+    int len_k, lim0;    // keys of the sequence; last key the first token sees
+    int t0, nt;
+    int two;            // two tiles of query rows
+    int tail;           // keys below len_k in the last key tile
+    int dest;           // -1: the rows' results, else partial result `dest` of this CTA
+    int pad;
+};
+
+__device__ __forceinline__ Seg make_seg(const SegWalk &w, const SchedGeom &g) {
+    Seg s;
+    s.row0 = w.s.q0 + w.tok0;
+    s.ntok = min(g.unit_tokens, w.s.new_q - w.tok0);
+    s.h = w.h;
+    s.b = w.b;
+    s.len_k = w.s.len_k;
+    s.lim0 = w.tok0 + w.s.len_k - w.s.new_q;
+    s.t0 = w.t0;
+    s.nt = w.t1 - w.t0;
+    s.two = w.two;
+    s.tail = min(g.tile, w.s.len_k - (w.t1 - 1) * g.tile);
+    s.dest = w.whole() ? -1 : (w.t0 == 0 ? 1 : 0);
+    s.pad = 0;
+    return s;
+}
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    } else {
+        __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+// Where key tiles lie in shared memory: groups of eight rows, in each the row's
+// 64-value column blocks one after the other, in each of those eight rows of 128
+// bytes, swizzled.  So a box of any multiple of eight rows and the whole head is
+// one piece, and one TMA copy: a copy costs the issuing warp some 75 cycles
+// whatever its size, and 16-row pages in copies of half a head were bound by that.
+template <int D>
+struct KeyTile {
+    static constexpr int kChunks = D / 64;
+    static constexpr int kGroupBytes = kChunks * 1024;      // eight rows
+    static constexpr int kBytes = 16 * kGroupBytes;         // 128 rows
+    // K (or V^T's columns): 16 values (32 bytes) per step along the row
+    __device__ static __forceinline__ uint64_t k_desc(uint32_t addr) { return smem_desc_sw128(addr, 16, kGroupBytes); }
+    __device__ static constexpr uint32_t k_step(int kk) { return ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4; }
+    // V: 16 keys per step; column blocks of 64 are 1024 bytes apart (`blocks` false:
+    // the one block again and again)
+    __device__ static __forceinline__ uint64_t v_desc(uint32_t addr, bool blocks) {
+        return smem_desc_sw128(addr, blocks ? 1024 : 0, kGroupBytes);
+    }
+    __device__ static constexpr uint32_t v_step(int kk) { return (kk * 2 * kGroupBytes) >> 4; }
+    // Rows [from, 128) = 0, by one warp.
+    __device__ static __forceinline__ void clear(uint8_t *tile, int from, int lane) {
+        for (int e = lane; e < (128 - from) * kChunks * 8; e += 32) {
+            const int r = from + e / (kChunks * 8), c = e % (kChunks * 8);
+            *reinterpret_cast<uint4 *>(tile + (r >> 3) * kGroupBytes + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+    }
+};
+
+// A lane's part of the copies of a key tile: box `lane` of it.  The table's entry
+// is asked for a tile ahead.
+struct PageBoxes {
+    const int *table;
+    int h, key_off;
+    bool copies;
+    int entry, row;
+
+    __device__ __forceinline__ void init(const PagedFwdParams &p, int lane) {
+        key_off = lane * p.box;
+        copies = key_off < 128;
+    }
+    __device__ __forceinline__ void segment(const PagedFwdParams &p, const Seg &s) {
+        table = p.kv.table + s.b * p.kv.table_stride;
+        h = s.h;
+    }
+    __device__ __forceinline__ void look_up(const PagedFwdParams &p, int kt, int len_k) {
+        const int key = kt * 128 + key_off;
+        entry = -1;
+        row = 0;
+        if (copies && key < len_k) {
+            const int pi = key / p.kv.page_size;
+            row = key - pi * p.kv.page_size;
+            entry = __ldg(table + pi);
+        }
+    }
+    // Coordinates of the box (dimensions: 64 values, 8 rows, column blocks, and
+    // either groups of eight rows and (page, head), or head and page).  A page that
+    // is not to be read is one past the last: TMA fills its box with zeros.
+    struct Box {
+        int y, z, w;
+    };
+    __device__ __forceinline__ Box box(const PagedFwdParams &p, int ratio) const {
+        const bool ok = entry >= 0 && entry < p.kv.num_pages;
+        if (p.fold) return Box{0, row >> 3, ok ? entry * ratio + h : (p.kv.num_pages - 1) * ratio + p.kv.Hkv};
+        return Box{row, h, ok ? entry : p.kv.num_pages};
+    }
+    __device__ __forceinline__ void copy(const PagedFwdParams &p, const CUtensorMap *m, uint32_t tile, int group_bytes,
+                                         uint32_t bar, const Box &b) const {
+        if (copies) tma_load_5d(tile + (key_off >> 3) * group_bytes, m, bar, 0, b.y, 0, b.z, b.w);
+    }
+};
+
+// Rows without a visible key: O = 0, LSE = -inf.  By one warp.
+template <int D>
+__device__ __forceinline__ void write_empty(const PagedFwdParams &p, int row0, int ntok, int h, int lane) {
+    const int n = ntok * p.G;
+    for (int r = lane; r < n; r += 32) {
+        const int t = row0 + r / p.G, head = h * p.G + r % p.G;
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + head * p.o_h + t * p.o_n);
+        for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
+        p.lse[static_cast<long long>(head) * p.T + t] = neg_inf();
+    }
+}
 
 }  // namespace fa

@@ -16,15 +16,18 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
-from . import FA_ERR_UNSUPPORTED, FaError, _bad, _check, _dtype_code, _stream_ptr, lib
+from . import FA_ERR_UNSUPPORTED, FA_OK, FaError, _bad, _check, _dtype_code, _stream_ptr, lib
 
 __all__ = ["Rope", "PagedKV", "rope_inv_freq", "fa_rope", "fa_rope_bwd", "rope_forward", "rope_backward",
            "fa_paged_append", "fa_paged_fwd", "fa_paged_fwd_workspace_bytes", "paged_attention", "paged_step",
            "rope_attention_forward", "rope_attention_backward"]
 
-_LL2 = ctypes.c_longlong * 2
 _LL3 = ctypes.c_longlong * 3
+# host arrays of strides, as the bytes that the C side reads during the call
+_strides2 = struct.Struct("2q").pack
+_strides3 = struct.Struct("3q").pack
 
 
 class _RopeSpec(ctypes.Structure):
@@ -177,29 +180,28 @@ class PagedKV:
 
 def _on_current(what, device):
     import torch
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         _bad(what, f"every tensor must be on the current device cuda:{torch.cuda.current_device()}, got {device}")
 
 
-def _rows(what, name, t, shape, dtype, device, out=False):
+def _rows(what, name, t, shape, dtype, device, low=0):
     """Check a 16-bit tensor whose last dimension is contiguous; its other
-    strides must be multiples of 8 elements (an output's rows must not overlap,
-    so at least D)."""
+    strides must be multiples of 8 elements and at least `low` (an output's rows
+    must not overlap, so D).  Returns its address and strides."""
     if t is None:
         _bad(what, f"{name} is required")
-    if tuple(t.shape) != shape:
-        _bad(what, f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.shape != shape:
+        _bad(what, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
         _bad(what, f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         _bad(what, f"{name} must be on {device}, got {t.device}")
     st = t.stride()
     if st[-1] != 1:
         _bad(what, f"{name} rows must be contiguous")
-    low = shape[-1] if out else 0
-    for n, s in zip(shape[:-1], st):
-        if n > 1 and (s & 7 or s < low):
-            _bad(what, f"{name} strides must be multiples of 8" + (" and at least D" if out else ""))
+    for n, s in zip(shape, st[:-1]):
+        if (s & 7 or s < low) and n > 1:
+            _bad(what, f"{name} strides must be multiples of 8" + (" and at least D" if low else ""))
     ptr = t.data_ptr()
     if ptr & 15:
         _bad(what, f"{name} must start 16-byte aligned")
@@ -236,7 +238,7 @@ def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream):
         _bad(what, "q must be [B, H, N, D] or [H, total, D]")
     code = _dtype_code(q)
     _need_rope(what, rope)
-    shape = tuple(q.shape)
+    shape = q.shape
     D, N, B = shape[-1], shape[-2], shape[0] if len(shape) == 4 else 1
     if rope.rot_dim > D:
         _bad(what, f"rot_dim {rope.rot_dim} exceeds D {D}")
@@ -245,28 +247,32 @@ def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream):
     if not q.is_cuda:
         _bad(what, f"every tensor must be on a CUDA device, got {q.device}")
     _on_current(what, q.device)
+    offset = int(offset)
     if rope.device != q.device:
         _bad(what, f"rope must be on {q.device}, got {rope.device}")
-    three = (lambda st: _LL3(*st[:3])) if len(shape) == 4 else (lambda st: _LL3(0, *st[:2]))
-    qp, qs = _rows(what, "q", q, shape, q.dtype, q.device)
-    qop, qos = _rows(what, "q_out", q_out, shape, q.dtype, q.device, out=True)
+    dtype, device = q.dtype, q.device
+    qp, qs = _rows(what, "q", q, shape, dtype, device)
+    qop, qos = _rows(what, "q_out", q_out, shape, dtype, device, D)
     Hk, kp, kop, ks, kos = 0, None, None, None, None
     if k is not None:
         if k.dim() != len(shape):
             _bad(what, "k must have as many dimensions as q")
         Hk = k.shape[-3]
         kshape = (*shape[:-3], Hk, N, D)
-        kp, ks = _rows(what, "k", k, kshape, q.dtype, q.device)
-        kop, kos = _rows(what, "k_out", k_out, kshape, q.dtype, q.device, out=True)
+        kp, ks = _rows(what, "k", k, kshape, dtype, device)
+        kop, kos = _rows(what, "k_out", k_out, kshape, dtype, device, D)
         if Hk == 0:
             kp = kop = ks = kos = None
     elif k_out is not None:
         _bad(what, "k_out without k")
-    pp, pstride = _positions(what, positions, B, N, q.device)
+    pp, pstride = _positions(what, positions, B, N, device)
     f = lib().fa_rope if what == "fa_rope" else lib().fa_rope_bwd
-    st = f(qp, three(qs), qop, three(qos), shape[-3], kp, ks and three(ks), kop, kos and three(kos), Hk, B, N, D,
-           rope._ref, pp, pstride, int(offset), code, _stream_ptr(stream))
-    _check(st, what)
+    # [B, H, N, D] has three strides beside the values', packed rows [H, total, D] two
+    three = (lambda st: st and _strides3(*st[:3])) if len(shape) == 4 else (lambda st: st and _strides3(0, *st[:2]))
+    st = f(qp, three(qs), qop, three(qos), shape[-3], kp, three(ks), kop, three(kos), Hk, B, N, D, rope._ref, pp,
+           pstride, offset, code, _stream_ptr(stream))
+    if st != FA_OK:
+        _check(st, what)
 
 
 def fa_rope(q, k, q_out, k_out, rope, positions=None, offset=0, stream=None):
@@ -369,14 +375,15 @@ def fa_paged_append(kv, k, v, cu_seqlens_q, rope=None, positions=None, q=None, q
             _bad(what, "q must be [Hq, total_q, D]")
         H = q.shape[0]
         qp, st = _rows(what, "q", q, (H, T, D), kv.dtype, kv.device)
-        qs = _LL2(st[0], st[1])
-        qop, st = _rows(what, "q_out", q_out, (H, T, D), kv.dtype, kv.device, out=True)
-        qos = _LL2(st[0], st[1])
+        qs = _strides2(st[0], st[1])
+        qop, st = _rows(what, "q_out", q_out, (H, T, D), kv.dtype, kv.device, D)
+        qos = _strides2(st[0], st[1])
     elif q_out is not None:
         _bad(what, "q_out without q")
-    st = lib().fa_paged_append(kv._ref, kp, _LL2(ks[0], ks[1]), vp, _LL2(vs[0], vs[1]), cup, T, ref, pp, qp, qs, qop,
+    st = lib().fa_paged_append(kv._ref, kp, _strides2(ks[0], ks[1]), vp, _strides2(vs[0], vs[1]), cup, T, ref, pp, qp, qs, qop,
                                qos, H, _stream_ptr(stream))
-    _check(st, what)
+    if st != FA_OK:
+        _check(st, what)
 
 
 def fa_paged_fwd_workspace_bytes(kv, Hq, max_seqlen_q) -> int:
@@ -398,9 +405,9 @@ def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=Tr
     if H % kv.num_kv_heads or not 1 <= H // kv.num_kv_heads <= 128:
         _bad(what, f"Hq must be 1 to 128 times the cache's {kv.num_kv_heads} heads, got {H}")
     shape = (H, T, kv.D)
-    qp, qs = _rows(what, "q", q, shape, kv.dtype, kv.device, out=True)
-    op, os_ = _rows(what, "o", o, shape, kv.dtype, kv.device, out=True)
-    if lse is None or tuple(lse.shape) != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    qp, qs = _rows(what, "q", q, shape, kv.dtype, kv.device, D)
+    op, os_ = _rows(what, "o", o, shape, kv.dtype, kv.device, D)
+    if lse is None or lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
         _bad(what, f"lse must be a contiguous torch.float32 tensor of shape {(H, T)}")
     if lse.device != kv.device:
         _bad(what, f"lse must be on {kv.device}, got {lse.device}")
@@ -409,11 +416,12 @@ def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=Tr
     if max_seqlen_q < 0:
         _bad(what, "max_seqlen_q must be >= 0")
     cup = _cu(what, kv, cu_seqlens_q)
-    st = lib().fa_paged_fwd(kv._ref, qp, _LL2(qs[0], qs[1]), op, _LL2(os_[0], os_[1]), lse.data_ptr(), cup, T,
+    st = lib().fa_paged_fwd(kv._ref, qp, _strides2(qs[0], qs[1]), op, _strides2(os_[0], os_[1]), lse.data_ptr(), cup, T,
                             int(max_seqlen_q), H, int(bool(causal)),
                             1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(),
                             workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    _check(st, what)
+    if st != FA_OK:
+        _check(st, what)
 
 
 def paged_attention(kv, q, cu_seqlens_q, max_seqlen_q, causal=True, scale=None, stream=None):
