@@ -44,7 +44,7 @@ namespace fa {
 namespace {
 
 constexpr int kBM = 128;            // query rows per tile
-constexpr int kBN = 128;            // keys per tile
+constexpr int kBN = kPagedTile;     // keys per tile
 constexpr int kThreads = 384;       // three warpgroups
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
@@ -120,7 +120,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const int lane = threadIdx.x & 31;
 
     PlanSeqs seqs;
-    if (warp == kPlanWarp) plan_load(p, lane, seqs);    // the tables arrive during the set-up
+    if (warp == kPlanWarp) plan_load(p, 0, lane, seqs);    // the tables arrive during the set-up
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
         tmem_relinquish();
@@ -694,21 +694,32 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
     if (m != neg_inf()) {
-#pragma unroll 4
-        for (int i = c; i <= mm.last; ++i) {
-            const float w = ex2_approx(p.lse_part[index(i)] - m);   // -inf: 0
-            const float *src = p.o_part + index(i) * D + lane * kPer;
-            sum += w;
-            if constexpr (kPer == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(src);
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
-                acc[2] = fmaf(w, v.z, acc[2]);
-                acc[3] = fmaf(w, v.w, acc[3]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(src);
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
+        for (int i0 = c; i0 <= mm.last; i0 += 32) {
+            // lane k has the weight of part i0 + k; the parts' rows kU at a time
+            constexpr int kU = 8;
+            const int cnt = min(32, mm.last + 1 - i0);
+            const float wl = lane < cnt ? ex2_approx(p.lse_part[index(i0 + lane)] - m) : 0.f;     // -inf: 0
+            for (int k = 0; k < cnt; k += kU) {
+                float w[kU], v[kU][kPer];
+#pragma unroll
+                for (int q = 0; q < kU; ++q) {
+                    w[q] = __shfl_sync(0xffffffffu, wl, (k + q) & 31);
+                    const float *src = p.o_part + index(i0 + min(k + q, cnt - 1)) * D + lane * kPer;
+                    if constexpr (kPer == 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(src);
+                        v[q][0] = f.x; v[q][1] = f.y; v[q][2] = f.z; v[q][3] = f.w;
+                    } else {
+                        const float2 f = *reinterpret_cast<const float2 *>(src);
+                        v[q][0] = f.x; v[q][1] = f.y;
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kU; ++q) {
+                    if (k + q >= cnt) break;
+                    sum += w[q];
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w[q], v[q][e], acc[e]);
+                }
             }
         }
     }

@@ -130,7 +130,6 @@ int check_cache(const fa_paged_kv *kv, fa::PagedCache *c) {
 // (a token has G rows, one per head of the group) and a unit of two tiles.
 fa::SchedGeom sched_geom(int G, int max_q) {
     fa::SchedGeom g;
-    g.tile = 128;
     g.tile_tokens = std::max(1, std::min(128 / G, max_q));
     g.unit_tokens = std::max(1, std::min(2 * (128 / G), max_q));
     if (max_q * G <= fa::kPagedTokenRows) g.tile_tokens = g.unit_tokens;    // one unit per sequence and kv head

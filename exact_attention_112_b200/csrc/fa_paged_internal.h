@@ -83,8 +83,9 @@ __host__ __device__ inline PagedSeq paged_seq(int b, const int *cu, const int *s
 }
 
 // Shape of the work units (fa_paged_sched.cuh).
+constexpr int kPagedTile = 128;         // keys per tile
+
 struct SchedGeom {
-    int tile;           // keys per tile
     int unit_tokens;    // tokens per unit
     int tile_tokens;    // tokens per tile of query rows (a unit past it has two)
     int one_cost, two_cost;     // entries that a key tile of a unit of one or two row tiles counts

@@ -32,7 +32,7 @@ __device__ __forceinline__ int unit_tiles(const PagedSeq &s, int tok0, const Sch
         const int last = min(tok0 + g.unit_tokens, s.new_q) - 1;
         vis = min(vis, last + 1 + s.len_k - s.new_q);
     }
-    return vis <= 0 ? 0 : (vis + g.tile - 1) / g.tile;
+    return vis <= 0 ? 0 : (vis + kPagedTile - 1) / kPagedTile;
 }
 
 __device__ __forceinline__ long long unit_cost(const PagedSeq &s, int tok0, const SchedGeom &g, int causal) {
@@ -70,35 +70,42 @@ struct Piece {
     PagedSeq s;             // its rows and keys
 };
 
-// The CTA's piece, computed by one warp (every lane gets the same).  A lane takes
-// every 32nd sequence; the first kPlanRounds of them stay in registers between
-// the sum and the search, so that a batch of up to 256 sequences costs one
-// latency of the tables.  min_piece: the least entries worth a CTA of its own.
-constexpr int kPlanRounds = 8;
+// The CTA's piece, computed by one warp (every lane gets the same) in steps of
+// 128 sequences, four to a lane; a batch of that size costs one latency of the
+// tables.  min_piece: the least entries worth a CTA of its own.
+constexpr int kPlanRounds = 4;
+constexpr int kPlanStep = 32 * kPlanRounds;
 
 struct PlanSeqs {
     PagedSeq s[kPlanRounds];
 };
 
-// The tables' part, to be asked for ahead of other set-up.
-__device__ __forceinline__ void plan_load(const PagedFwdParams &p, int lane, PlanSeqs &q) {
-#pragma unroll
-    for (int i = 0; i < kPlanRounds; ++i)
-        q.s[i] = 32 * i + lane < p.kv.num_seqs ? load_seq(p, 32 * i + lane) : PagedSeq{0, 0, 0};
-}
-
-__device__ __forceinline__ Piece plan_piece(const PagedFwdParams &p, const SchedGeom &g, int min_piece, int lane,
-                                            const PlanSeqs &q) {
-    const int B = p.kv.num_seqs;
-    auto cost = [&](const PagedSeq &s) { return p.kv.Hkv * head_cost(s, g, p.causal); };
-    Piece pc;
-    long long mine[kPlanRounds], v = 0;
+__device__ __forceinline__ void plan_load(const PagedFwdParams &p, int b0, int lane, PlanSeqs &q) {
 #pragma unroll
     for (int i = 0; i < kPlanRounds; ++i) {
-        mine[i] = 32 * i < B ? cost(q.s[i]) : 0;
-        v += mine[i];
+        const int b = b0 + 32 * i + lane;
+        q.s[i] = b < p.kv.num_seqs ? load_seq(p, b) : PagedSeq{0, 0, 0};
     }
-    for (int b = 32 * kPlanRounds + lane; b < B; b += 32) v += cost(load_seq(p, b));
+}
+
+// q: sequences 0 .. kPlanStep - 1, asked for by the caller ahead of other set-up.
+__device__ __forceinline__ Piece plan_piece(const PagedFwdParams &p, const SchedGeom &g, int min_piece, int lane,
+                                            PlanSeqs &q) {
+    const int B = p.kv.num_seqs;
+    Piece pc;
+    long long mine[kPlanRounds], v = 0;
+    auto costs = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < kPlanRounds; ++i) {
+            mine[i] = b0 + 32 * i < B ? p.kv.Hkv * head_cost(q.s[i], g, p.causal) : 0;
+            v += mine[i];
+        }
+    };
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += kPlanStep) {
+        if (b0 > 0) plan_load(p, b0, lane, q);
+        costs(b0);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     pc.total = v;
@@ -113,31 +120,33 @@ __device__ __forceinline__ Piece plan_piece(const PagedFwdParams &p, const Sched
     pc.lo = c * pc.quot + min(c, pc.rem);
     pc.hi = pc.lo + pc.quot + (c < pc.rem ? 1 : 0);
     long long base = 0;     // entries before the round's sequences
-    auto round = [&](int b0, long long mine_b, const PagedSeq &s) {
-        long long inc = mine_b;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += kPlanStep) {
+        if (B > kPlanStep) {
+            plan_load(p, b0, lane, q);
+            costs(b0);
         }
-        const long long at = base + inc - mine_b;
-        const unsigned hit = __ballot_sync(0xffffffffu, mine_b > 0 && at <= pc.lo && pc.lo < at + mine_b);
-        base += __shfl_sync(0xffffffffu, inc, 31);
-        if (hit == 0) return false;
-        const int l = __ffs(hit) - 1;
-        pc.b = b0 + l;
-        pc.start = __shfl_sync(0xffffffffu, at, l);
-        pc.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
-        pc.s.new_q = __shfl_sync(0xffffffffu, s.new_q, l);
-        pc.s.len_k = __shfl_sync(0xffffffffu, s.len_k, l);
-        return true;
-    };
 #pragma unroll
-    for (int i = 0; i < kPlanRounds; ++i)
-        if (32 * i < B && round(32 * i, mine[i], q.s[i])) return pc;
-    for (int b0 = 32 * kPlanRounds; b0 < B; b0 += 32) {
-        const PagedSeq s = b0 + lane < B ? load_seq(p, b0 + lane) : PagedSeq{0, 0, 0};
-        if (round(b0, cost(s), s)) return pc;
+        for (int i = 0; i < kPlanRounds; ++i) {
+            if (b0 + 32 * i >= B) break;
+            long long inc = mine[i];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            const long long at = base + inc - mine[i];
+            const unsigned hit = __ballot_sync(0xffffffffu, mine[i] > 0 && at <= pc.lo && pc.lo < at + mine[i]);
+            base += __shfl_sync(0xffffffffu, inc, 31);
+            if (hit == 0) continue;
+            const int l = __ffs(hit) - 1;
+            pc.b = b0 + 32 * i + l;
+            pc.start = __shfl_sync(0xffffffffu, at, l);
+            pc.s.q0 = __shfl_sync(0xffffffffu, q.s[i].q0, l);
+            pc.s.new_q = __shfl_sync(0xffffffffu, q.s[i].new_q, l);
+            pc.s.len_k = __shfl_sync(0xffffffffu, q.s[i].len_k, l);
+            return pc;
+        }
     }
     return pc;
 }
@@ -247,7 +256,7 @@ __device__ __forceinline__ Seg make_seg(const SegWalk &w, const SchedGeom &g) {
     s.t0 = w.t0;
     s.nt = w.t1 - w.t0;
     s.two = w.two;
-    s.tail = min(g.tile, w.s.len_k - (w.t1 - 1) * g.tile);
+    s.tail = min(kPagedTile, w.s.len_k - (w.t1 - 1) * kPagedTile);
     s.dest = w.whole() ? -1 : (w.t0 == 0 ? 1 : 0);
     s.pad = 0;
     return s;

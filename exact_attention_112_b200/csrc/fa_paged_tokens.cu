@@ -17,7 +17,8 @@
 // more than 2^8, which one vote over the warpgroup finds out; the row sums stay
 // spread over the threads until the unit's end.
 //
-// Warps: 0-3 softmax, 4 TMA (each lane looks up the page of its box), 5 MMA, 6
+// Warps: one warpgroup of softmax (two for R = 64, half of the rows each), then a
+// TMA warp (each lane looks up the page of its box), an MMA warp, and one that
 // walks the CTA's share of the work (fa_paged_sched.cuh).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -32,13 +33,10 @@
 namespace fa {
 namespace {
 
-constexpr int kBN = 128;            // keys per tile
-constexpr int kThreads = 256;
-constexpr int kProducerWarp = 4;
-constexpr int kMmaWarp = 5;
-constexpr int kPlanWarp = 6;
+constexpr int kBN = kPagedTile;     // keys per tile
 constexpr int kDescs = 8;           // segment descriptors in the ring
 constexpr float kTau = 8.0f;        // a row's reference maximum moves past this (log2 units)
+constexpr float kNone = -1e30f;     // reference maximum of a row that has seen no key
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // What the threads share of a row, beside its reference maximum: the factor that
@@ -51,6 +49,12 @@ struct alignas(16) RowState {
 
 template <int D, int R>
 struct TokenLayout {
+    static constexpr int kGroups = R == 64 ? 2 : 1;       // softmax warpgroups
+    static constexpr int kCols = R / kGroups;             // rows of each
+    static constexpr int kProducerWarp = 4 * kGroups;
+    static constexpr int kMmaWarp = kProducerWarp + 1;
+    static constexpr int kPlanWarp = kProducerWarp + 2;
+    static constexpr int kThreads = 32 * (kProducerWarp + 4);
     static constexpr int kChunks = D / 64;                // 128-byte column blocks per row
     static constexpr int kTileBytes = KeyTile<D>::kBytes;
     static constexpr int kQChunk = R * 128;
@@ -81,7 +85,7 @@ struct TokenLayout {
     static constexpr int kNumBars = kVEmpty + kVStages;
     static constexpr int kMisc = kBar + kNumBars * 8;     // tensor-memory base, abort flag
     static constexpr int kDesc = (kMisc + 8 + 15) / 16 * 16;
-    static constexpr int kRed = kDesc + kDescs * static_cast<int>(sizeof(Seg));     // float [4][R]
+    static constexpr int kRed = kDesc + kDescs * static_cast<int>(sizeof(Seg));     // float [warp][kCols]
     static constexpr int kRow = kRed + 4 * R * 4;         // RowState [R]
     static constexpr int kMax = kRow + R * 16;            // float [R]: reference maxima
     static constexpr int kBytes = kMax + R * 4;
@@ -91,11 +95,10 @@ struct TokenLayout {
     static_assert(kAlloc <= 231424, "shared memory");
 };
 
-template <int R>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[R]) {
-    if constexpr (R == 16) tmem_ld32dp_x16_wait(taddr, r);
-    else if constexpr (R == 32) tmem_ld32dp_x32_wait(taddr, r);
-    else tmem_ld32dp_x64_wait(taddr, r);
+template <int C>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[C]) {
+    if constexpr (C == 16) tmem_ld32dp_x16_wait(taddr, r);
+    else tmem_ld32dp_x32_wait(taddr, r);
 }
 
 // The warp's maxima (or sums) of N = 16 or 32 values per lane, N - 1 (+ 1)
@@ -125,15 +128,14 @@ __device__ __forceinline__ float warp_reduce_rows(const float *x, int lane) {
     return v[0];
 }
 
-// Per warp and row, into red[warp][row].
-template <int R, bool MAX>
-__device__ __forceinline__ void reduce_rows(const float (&x)[R], float *red, int warp, int lane) {
-    if constexpr (R == 16) {
-        const float v = warp_reduce_rows<16, MAX>(x, lane);
-        if ((lane & 1) == 0) red[warp * R + (lane >> 1)] = v;
+// Per warp and row, into red[row].
+template <int C, bool MAX>
+__device__ __forceinline__ void reduce_rows(const float (&x)[C], float *red, int lane) {
+    const float v = warp_reduce_rows<C, MAX>(x, lane);
+    if constexpr (C == 16) {
+        if ((lane & 1) == 0) red[lane >> 1] = v;
     } else {
-#pragma unroll
-        for (int h = 0; h < R / 32; ++h) red[warp * R + 32 * h + lane] = warp_reduce_rows<32, MAX>(x + 32 * h, lane);
+        red[lane] = v;
     }
 }
 
@@ -144,11 +146,13 @@ __device__ __forceinline__ uint16_t round16(float x) {
 }
 
 template <int D, int R, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TokenLayout<D, R>::kThreads, 1)
 fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedFwdParams p) {
     using L = TokenLayout<D, R>;
     using KT = KeyTile<D>;
+    constexpr int kProducerWarp = L::kProducerWarp, kMmaWarp = L::kMmaWarp, kPlanWarp = L::kPlanWarp;
+    constexpr int kThreads = L::kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -157,15 +161,12 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     Seg *descs = reinterpret_cast<Seg *>(smem + L::kDesc);
-    float *red = reinterpret_cast<float *>(smem + L::kRed);
-    RowState *row_state = reinterpret_cast<RowState *>(smem + L::kRow);
-    float *m_ref = reinterpret_cast<float *>(smem + L::kMax);      // log2 units
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
     PlanSeqs seqs;
-    if (warp == kPlanWarp) plan_load(p, lane, seqs);    // the tables arrive during the set-up
+    if (warp == kPlanWarp) plan_load(p, 0, lane, seqs);    // the tables arrive during the set-up
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
         tmem_relinquish();
@@ -176,13 +177,13 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             mbar_init(bar(L::kQFull + i), 1);
             mbar_init(bar(L::kQEmpty + i), 1);
             mbar_init(bar(L::kSFull + i), 1);
-            mbar_init(bar(L::kPFull + i), 128);
+            mbar_init(bar(L::kPFull + i), 128 * L::kGroups);
             mbar_init(bar(L::kPvDone + i), 1);
         }
         mbar_init(bar(L::kDrain), 1);
         for (int i = 0; i < kDescs; ++i) {
             mbar_init(bar(L::kDFull + i), 1);
-            mbar_init(bar(L::kDEmpty + i), 6);       // producer, MMA and four softmax warps
+            mbar_init(bar(L::kDEmpty + i), 2 + 4 * L::kGroups);      // producer, MMA, softmax warps
         }
         for (int s = 0; s < L::kKStages; ++s) {
             mbar_init(bar(L::kKFull + s), 1);
@@ -395,51 +396,59 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
-    } else if (warp < 4) {
+    } else if (warp < kProducerWarp) {
         // ===================== softmax =====================
-        const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const int key = warp * 32 + lane;           // within the tile
+        constexpr int C = L::kCols;
+        const int wg = warp >> 2, wq = warp & 3;    // warpgroup, lane quarter of tensor memory
+        const uint32_t wg_bar = 2 + wg;
+        const int key = wq * 32 + lane;             // within the tile
+        const int row0 = wg * C;                    // first row of the warpgroup's
+        const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16) + row0;
+        float *const red = reinterpret_cast<float *>(smem + L::kRed) + wg * 4 * C;
+        RowState *const row_state = reinterpret_cast<RowState *>(smem + L::kRow) + row0;
+        float *const m_ref = reinterpret_cast<float *>(smem + L::kMax) + row0;      // log2 units
         const float qk = p.qk_scale_log2;
         // this key's place in row r of P: column block, then 16-byte units swizzled by the row
-        uint8_t *const p_key = smem + L::kP + (key >> 6) * L::kQChunk + (key & 7) * 2;
+        uint8_t *const p_key = smem + L::kP + (key >> 6) * L::kQChunk + row0 * 128 + (key & 7) * 2;
         const int p_unit = (key & 63) >> 3;
         // P V of key tile t and all before it.  Its barrier serves every other tile:
-        // a wait can tell a phase only from the one before, and S(t + 1), seen
-        // before any such wait, covers the products up to t - 2.
+        // a wait can tell a phase only from the one before, and S(t), seen before any
+        // such wait, covers the products up to t - 2.
         auto wait_pv = [&](int t) { return mbar_wait_warp(bar(L::kPvDone + (t & 1)), (t >> 1) & 1, wctx); };
         int t = 0;                                  // key tiles so far
         bool ok = true;
         for (int u = 0; ok; ++u) {
             if (!desc_wait(u)) ok = false;
-            if (key < R) m_ref[key] = neg_inf();    // row r's state is thread r's to write, everyone's to read
+            if (key < C) m_ref[key] = kNone;        // row r's state is thread r's to write, everyone's to read
             // one outcome for the four warps: they meet at barriers below
-            if (named_bar_or(2, 128, !ok)) { ok = false; break; }
+            if (named_bar_or(wg_bar, 128, !ok)) { ok = false; break; }
             const Seg &s = descs[u % kDescs];
             if (s.nt == 0) break;
-            const int nt = s.nt, rows = s.ntok * p.G, len_k = s.len_k;
+            const int nt = s.nt, len_k = s.len_k;
             const int edge = p.causal ? min(s.lim0, len_k - 1) : len_k - 1;   // keys up to it are seen by all rows
-            // Rows past `rows` compute like the others, from what Q's buffer holds,
-            // and are not stored; a product's columns do not mix.
-            float l[R];                             // this thread's keys only
+            // Rows past the segment's compute like the others, from what Q's buffer
+            // holds, and are not stored; a product's columns do not mix.
+            float l[C];                             // this thread's keys only
 #pragma unroll
-            for (int r = 0; r < R; ++r) l[r] = 0.f;
+            for (int r = 0; r < C; ++r) l[r] = 0.f;
             for (int j = 0; j < nt; ++j, ++t) {
                 const int kv = (s.t0 + j) * kBN + key;
                 const bool got = mbar_wait_warp(bar(L::kSFull + (t & 1)), (t >> 1) & 1, wctx);
                 tc_fence_after();
-                float x[R];
+                float x[C];                         // scores, not scaled
                 {
-                    uint32_t sr[R];
-                    tmem_ld_cols<R>(tl + L::kColS + (t & 1) * R, sr);
+                    uint32_t sr[C];
+                    tmem_ld_cols<C>(tl + L::kColS + (t & 1) * R, sr);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) x[r] = __uint_as_float(sr[r]) * qk;
+                    for (int r = 0; r < C; ++r) x[r] = __uint_as_float(sr[r]);
                 }
                 if (kv - key + kBN - 1 > edge) {
                     // row r is the head r % G of token r / G, which sees one key
                     // more than the token before
-                    int lim = edge, g = 0, tok = 0;
+                    int tok = row0 / p.G, g = row0 - tok * p.G;
+                    int lim = p.causal ? min(s.lim0 + tok, len_k - 1) : edge;
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
+                    for (int r = 0; r < C; ++r) {
                         if (kv > lim) x[r] = neg_inf();
                         if (++g == p.G) {
                             g = 0;
@@ -448,33 +457,47 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                         }
                     }
                 }
-                bool need = !got;
+                // a = log2 of the probability, before l: x * qk - m_ref
+                float a[C];
+                auto subtract = [&]() {
 #pragma unroll
-                for (int r = 0; r < R; r += 4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(m_ref + r);
-                    need |= x[r] > m.x + kTau || x[r + 1] > m.y + kTau || x[r + 2] > m.z + kTau || x[r + 3] > m.w + kTau;
+                    for (int r = 0; r < C; r += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(m_ref + r);
+                        a[r] = fmaf(x[r], qk, -m.x);
+                        a[r + 1] = fmaf(x[r + 1], qk, -m.y);
+                        a[r + 2] = fmaf(x[r + 2], qk, -m.z);
+                        a[r + 3] = fmaf(x[r + 3], qk, -m.w);
+                    }
+                };
+                subtract();
+                float top = fmaxf(a[0], a[1]), top2 = fmaxf(a[2], a[3]);
+#pragma unroll
+                for (int r = 4; r < C; r += 4) {
+                    top = fmax3(top, a[r], a[r + 1]);
+                    top2 = fmax3(top2, a[r + 2], a[r + 3]);
                 }
-                if (named_bar_or(2, 128, need)) {
-                    if (named_bar_or(2, 128, !got)) { ok = false; break; }
-                    reduce_rows<R, true>(x, red, warp, lane);
-                    named_bar_sync(2, 128);
-                    if (key < R) {
-                        const float v = fmaxf(fmaxf(red[key], red[R + key]), fmaxf(red[2 * R + key], red[3 * R + key]));
+                if (named_bar_or(wg_bar, 128, !got || fmaxf(top, top2) > kTau)) {
+                    if (named_bar_or(wg_bar, 128, !got)) { ok = false; break; }
+                    reduce_rows<C, true>(x, red + wq * C, lane);
+                    named_bar_sync(wg_bar, 128);
+                    if (key < C) {
+                        const float v =
+                            qk * fmaxf(fmaxf(red[key], red[C + key]), fmaxf(red[2 * C + key], red[3 * C + key]));
                         const float m = m_ref[key];
                         const bool move = v > m + kTau;
                         m_ref[key] = move ? v : m;
-                        row_state[key].factor = !move ? 1.f : m == neg_inf() ? 0.f : ex2_approx(m - v);
+                        row_state[key].factor = move ? ex2_approx(m - v) : 1.f;     // kNone: 0
                     }
-                    named_bar_sync(2, 128);
+                    named_bar_sync(wg_bar, 128);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) l[r] *= row_state[r].factor;
+                    for (int r = 0; r < C; ++r) l[r] *= row_state[r].factor;
                     if (j > 0) {
                         // O's columns too, when the products so far are in it
                         const bool done = wait_pv(t - 1);
-                        if (named_bar_or(2, 128, !done)) { ok = false; break; }
+                        if (named_bar_or(wg_bar, 128, !done)) { ok = false; break; }
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < R; c += 16) {
+                        for (int c = 0; c < C; c += 16) {
                             uint32_t orr[16];
                             tmem_ld32dp_x16_wait(tl + L::kColO + c, orr);
 #pragma unroll
@@ -484,20 +507,19 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                         }
                         tmem_wait_st();
                     }
+                    subtract();
                 }
-                // P = 2^(x - m), rounded to the operands' type; masked keys give 0
+                // P = 2^a, rounded to the operands' type; masked keys give 0
                 uint8_t *const pt = p_key + (t & 1) * L::kPBytes;
 #pragma unroll
-                for (int r4 = 0; r4 < R; r4 += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4 *>(m_ref + r4);
-                    const float ms[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r4 + i;
-                        const float e = ex2_approx(x[r] - (ms[i] == neg_inf() ? 0.f : ms[i]));
-                        l[r] += e;
-                        *reinterpret_cast<uint16_t *>(pt + r * 128 + ((p_unit ^ (r & 7)) << 4)) = round16<BF16>(e);
-                    }
+                for (int r = 0; r < C; r += 2) {
+                    const float e0 = ex2_approx(a[r]), e1 = ex2_approx(a[r + 1]);
+                    l[r] += e0;
+                    l[r + 1] += e1;
+                    const uint32_t e = pack2<BF16>(e0, e1);
+                    *reinterpret_cast<uint16_t *>(pt + r * 128 + ((p_unit ^ (r & 7)) << 4)) = static_cast<uint16_t>(e);
+                    *reinterpret_cast<uint16_t *>(pt + (r + 1) * 128 + ((p_unit ^ ((r + 1) & 7)) << 4)) =
+                        static_cast<uint16_t>(e >> 16);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -506,14 +528,15 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             if (!ok) break;
 
             // ---- the rows' results
-            reduce_rows<R, false>(l, red, warp, lane);
+            reduce_rows<C, false>(l, red + wq * C, lane);
+            const int rows = min(C, s.ntok * p.G - row0);       // this warpgroup's (none: <= 0)
             const bool done = wait_pv(t - 1);
-            if (named_bar_or(2, 128, !done)) { ok = false; break; }
+            if (named_bar_or(wg_bar, 128, !done)) { ok = false; break; }
             if (key < rows) {
-                const float sum = (red[key] + red[R + key]) + (red[2 * R + key] + red[3 * R + key]);
+                const float sum = (red[key] + red[C + key]) + (red[2 * C + key] + red[3 * C + key]);
                 const float lse2 = sum > 0.f ? m_ref[key] + lg2_approx(sum) : neg_inf();
-                const int tok = key / p.G, head = s.h * p.G + key - tok * p.G;
-                const size_t part = (2 * blockIdx.x + s.dest) * static_cast<size_t>(p.part_rows) + key;
+                const int r = row0 + key, tok = r / p.G, head = s.h * p.G + r - tok * p.G;
+                const size_t part = (2 * blockIdx.x + s.dest) * static_cast<size_t>(p.part_rows) + r;
                 row_state[key].factor = sum > 0.f ? 1.f / sum : 0.f;
                 row_state[key].at = s.dest < 0 ? head * p.o_h + (s.row0 + tok) * p.o_n : static_cast<long long>(part) * D;
                 if (s.dest < 0)
@@ -521,33 +544,39 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 else
                     p.lse_part[part] = lse2;
             }
-            named_bar_sync(2, 128);
+            named_bar_sync(wg_bar, 128);
             tc_fence_after();
+            auto store_rows = [&](auto *out) {
 #pragma unroll 1
-            for (int c = 0; c < rows; c += 8) {
-                uint32_t orr[8];
-                tmem_ld32dp_x8_wait(tl + L::kColO + c, orr);
-                if (key < D) {
+                for (int c = 0; c < rows; c += 8) {
+                    uint32_t orr[8];
+                    tmem_ld32dp_x8_wait(tl + L::kColO + c, orr);
+                    RowState rs[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) rs[e] = row_state[c + e];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        if (c + e >= rows) break;
-                        const float y = __uint_as_float(orr[e]) * row_state[c + e].factor;
-                        if (s.dest < 0)
-                            static_cast<uint16_t *>(p.o)[row_state[c + e].at + key] = round16<BF16>(y);
-                        else
-                            p.o_part[row_state[c + e].at + key] = y;
+                        const float y = __uint_as_float(orr[e]) * rs[e].factor;
+                        if (key < D && c + e < rows) {
+                            if constexpr (sizeof(*out) == 2) out[rs[e].at + key] = round16<BF16>(y);
+                            else out[rs[e].at + key] = y;
+                        }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
-            }
+            };
+            if (s.dest < 0)
+                store_rows(static_cast<uint16_t *>(p.o));
+            else
+                store_rows(p.o_part);
             tc_fence_before();
-            named_bar_sync(2, 128);     // the rows' state is read, the next segment may replace it
+            named_bar_sync(wg_bar, 128);     // the rows' state is read, the next segment may replace it
             desc_release(u);
         }
         __syncwarp();
         named_bar_sync(1, kThreads);
     } else {
-        named_bar_sync(1, kThreads);    // warp 7
+        named_bar_sync(1, kThreads);    // the last warp
     }
 }
 
@@ -557,7 +586,7 @@ cudaError_t launch_t(const PagedTensorMaps &tm, const PagedFwdParams &p, int gri
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TokenLayout<D, R>::kAlloc);
     if (e != cudaSuccess) return e;
     prof_begin(stream, "fa_paged_tokens_kernel");
-    kern<<<grid, kThreads, TokenLayout<D, R>::kAlloc, stream>>>(tm.q, tm.k, tm.v, p);
+    kern<<<grid, TokenLayout<D, R>::kThreads, TokenLayout<D, R>::kAlloc, stream>>>(tm.q, tm.k, tm.v, p);
     prof_end(stream);
     note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
