@@ -40,10 +40,27 @@ __device__ __forceinline__ long long unit_cost(const PagedSeq &s, int tok0, cons
     return n * (tok0 + g.tile_tokens < s.new_q ? g.two_cost : g.one_cost);
 }
 
-// Work of one kv head of a sequence.
-__device__ __forceinline__ long long head_cost(const PagedSeq &s, const SchedGeom &g, int causal) {
+// Work of one kv head of each lane's sequence.  A sequence of many units is
+// summed up by the whole warp.
+__device__ __forceinline__ long long head_cost(const PagedSeq &s, const SchedGeom &g, int causal, int lane) {
+    const bool many = s.new_q > 2 * g.unit_tokens;
     long long c = 0;
-    for (int t = 0; t < s.new_q; t += g.unit_tokens) c += unit_cost(s, t, g, causal);
+    if (!many && s.new_q > 0) {
+        c = unit_cost(s, 0, g, causal);
+        if (s.new_q > g.unit_tokens) c += unit_cost(s, g.unit_tokens, g, causal);
+    }
+    for (unsigned todo = __ballot_sync(0xffffffffu, many); todo != 0; todo &= todo - 1) {
+        const int l = __ffs(todo) - 1;
+        PagedSeq w;
+        w.q0 = 0;
+        w.new_q = __shfl_sync(0xffffffffu, s.new_q, l);
+        w.len_k = __shfl_sync(0xffffffffu, s.len_k, l);
+        long long sum = 0;
+        for (int t = lane * g.unit_tokens; t < w.new_q; t += 32 * g.unit_tokens) sum += unit_cost(w, t, g, causal);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == l) c = sum;
+    }
     return c;
 }
 
@@ -68,6 +85,7 @@ struct Piece {
     long long start;        // first entry of sequence b
     int b;                  // sequence that holds entry lo (-1: no work)
     PagedSeq s;             // its rows and keys
+    long long per_head;     // its work for one kv head
 };
 
 // The CTA's piece, computed by one warp (every lane gets the same) in steps of
@@ -97,7 +115,7 @@ __device__ __forceinline__ Piece plan_piece(const PagedFwdParams &p, const Sched
     auto costs = [&](int b0) {
 #pragma unroll
         for (int i = 0; i < kPlanRounds; ++i) {
-            mine[i] = b0 + 32 * i < B ? p.kv.Hkv * head_cost(q.s[i], g, p.causal) : 0;
+            mine[i] = b0 + 32 * i < B ? p.kv.Hkv * head_cost(q.s[i], g, p.causal, lane) : 0;
             v += mine[i];
         }
     };
@@ -145,6 +163,7 @@ __device__ __forceinline__ Piece plan_piece(const PagedFwdParams &p, const Sched
             pc.s.q0 = __shfl_sync(0xffffffffu, q.s[i].q0, l);
             pc.s.new_q = __shfl_sync(0xffffffffu, q.s[i].new_q, l);
             pc.s.len_k = __shfl_sync(0xffffffffu, q.s[i].len_k, l);
+            pc.per_head = div_wide(__shfl_sync(0xffffffffu, mine[i], l), p.kv.Hkv);
             return pc;
         }
     }
@@ -172,7 +191,8 @@ struct SegWalk {
         cost = static_cast<long long>(w) * max(1, n);
     }
 
-    __device__ __forceinline__ void first(const PagedFwdParams &p, const SchedGeom &g, const Piece &pc) {
+    // By a whole warp: the unit that holds entry lo.
+    __device__ __forceinline__ void first(const PagedFwdParams &p, const SchedGeom &g, const Piece &pc, int lane) {
         lo = pc.lo;
         hi = pc.hi;
         b = pc.b;
@@ -180,15 +200,28 @@ struct SegWalk {
         tok0 = 0;
         base = pc.start;
         s = pc.s;
-        const long long per_head = head_cost(s, g, p.causal);
-        h = static_cast<int>(div_wide(lo - base, per_head));
-        base += h * per_head;
-        unit(p, g);
-        while (base + cost <= lo) {
-            base += cost;
-            tok0 += g.unit_tokens;
-            unit(p, g);
+        h = static_cast<int>(div_wide(lo - base, pc.per_head));
+        base += h * pc.per_head;
+        // 32 units at a time
+        for (;; tok0 += 32 * g.unit_tokens) {
+            const int t = tok0 + lane * g.unit_tokens;
+            const long long c = t < s.new_q ? unit_cost(s, t, g, p.causal) : 0;
+            long long inc = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, c > 0 && lo < base + inc);
+            if (hit != 0) {
+                const int l = __ffs(hit) - 1;
+                base += __shfl_sync(0xffffffffu, inc - c, l);
+                tok0 += l * g.unit_tokens;
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
         }
+        unit(p, g);
         range();
     }
 

@@ -235,7 +235,7 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             };
             if (pc.b >= 0) {
                 SegWalk w;
-                w.first(p, p.geom, pc);
+                w.first(p, p.geom, pc, lane);
                 do {
                     const Seg s = make_seg(w, p.geom);
                     if (w.n == 0) {

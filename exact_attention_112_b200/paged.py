@@ -14,6 +14,7 @@ them alive; the tables' values may change between calls, their storage may not.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import struct
@@ -208,6 +209,16 @@ def _rows(what, name, t, shape, dtype, device, low=0):
     return ptr, st
 
 
+def _allocating_on(stream):
+    """Context in which torch allocates for ``stream`` (the current one if None):
+    memory that a kernel of another stream fills must not come from, nor go back
+    to, the pool of the current one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _need_rope(what, rope):
     if not isinstance(rope, Rope):
         _bad(what, "rope must be a Rope")
@@ -290,8 +301,9 @@ def fa_rope_bwd(dq_out, dk_out, dq, dk, rope, positions=None, offset=0, stream=N
 def rope_forward(q, k, rope, positions=None, offset=0, stream=None):
     """Allocate the rotated q and k with torch and run ``fa_rope``."""
     import torch
-    q_out = torch.empty_like(q)
-    k_out = None if k is None else torch.empty_like(k)
+    with _allocating_on(stream):
+        q_out = torch.empty_like(q)
+        k_out = None if k is None else torch.empty_like(k)
     fa_rope(q, k, q_out, k_out, rope, positions=positions, offset=offset, stream=stream)
     return q_out, k_out
 
@@ -299,8 +311,9 @@ def rope_forward(q, k, rope, positions=None, offset=0, stream=None):
 def rope_backward(dq_out, dk_out, rope, positions=None, offset=0, stream=None):
     """Allocate dq and dk with torch and run ``fa_rope_bwd``."""
     import torch
-    dq = torch.empty_like(dq_out)
-    dk = None if dk_out is None else torch.empty_like(dk_out)
+    with _allocating_on(stream):
+        dq = torch.empty_like(dq_out)
+        dk = None if dk_out is None else torch.empty_like(dk_out)
     fa_rope_bwd(dq_out, dk_out, dq, dk, rope, positions=positions, offset=offset, stream=stream)
     return dq, dk
 
@@ -310,9 +323,10 @@ def rope_attention_forward(q, k, v, rope, positions=None, offset=0, causal=False
     """attention_forward of the rotated q and k; returns (o, lse, q_rot, k_rot),
     the last two for rope_attention_backward."""
     from . import attention_forward
-    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-    q_rot, k_rot = rope_forward(q, k, rope, positions=positions, offset=offset, stream=stream)
-    o, lse = attention_forward(q_rot, k_rot, v, causal=causal, scale=scale, key_bias=key_bias, stream=stream)
+    with _allocating_on(stream):
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        q_rot, k_rot = rope_forward(q, k, rope, positions=positions, offset=offset, stream=stream)
+        o, lse = attention_forward(q_rot, k_rot, v, causal=causal, scale=scale, key_bias=key_bias, stream=stream)
     return o, lse, q_rot, k_rot
 
 
@@ -321,8 +335,9 @@ def rope_attention_backward(q_rot, k_rot, v, o, lse, dO, rope, positions=None, o
     """Gradients of rope_attention_forward with respect to q, k (before the
     rotation) and v."""
     from . import attention_backward
-    dq, dk, dv = attention_backward(q_rot, k_rot, v.contiguous(), o, lse, dO, causal=causal, scale=scale,
-                                    key_bias=key_bias, stream=stream)
+    with _allocating_on(stream):
+        dq, dk, dv = attention_backward(q_rot, k_rot, v.contiguous(), o, lse, dO, causal=causal, scale=scale,
+                                        key_bias=key_bias, stream=stream)
     fa_rope_bwd(dq, dk, dq, dk, rope, positions=positions, offset=offset, stream=stream)
     return dq, dk, dv
 
@@ -430,9 +445,10 @@ def paged_attention(kv, q, cu_seqlens_q, max_seqlen_q, causal=True, scale=None, 
     if q is None or q.dim() != 3:
         _bad("fa_paged_fwd", "q must be [Hq, total_q, D]")
     _need_kv("fa_paged_fwd", kv)
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    ws = torch.empty(fa_paged_fwd_workspace_bytes(kv, q.shape[0], max_seqlen_q), dtype=torch.uint8, device=kv.device)
+    with _allocating_on(stream):
+        o = torch.empty_like(q)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        ws = torch.empty(fa_paged_fwd_workspace_bytes(kv, q.shape[0], max_seqlen_q), dtype=torch.uint8, device=kv.device)
     fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, ws, causal=causal, scale=scale, stream=stream)
     return o, lse
 
@@ -445,7 +461,8 @@ def paged_step(kv, q, k, v, cu_seqlens_q, max_seqlen_q, rope=None, positions=Non
     import torch
     q_rot = q
     if rope is not None:
-        q_rot = torch.empty_like(q)
+        with _allocating_on(stream):
+            q_rot = torch.empty_like(q)
         fa_paged_append(kv, k, v, cu_seqlens_q, rope=rope, positions=positions, q=q, q_out=q_rot, stream=stream)
     else:
         fa_paged_append(kv, k, v, cu_seqlens_q, stream=stream)
