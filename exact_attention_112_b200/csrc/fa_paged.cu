@@ -506,7 +506,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const float m_use = (m_ref == neg_inf()) ? 0.f : m_ref;
                 // p = 2^(x - m) in two halves of 64 keys, each handed to the MMA
                 // warp on its own barrier; one pair in kEmuEvery on the FMA pipe
-                // once every row has a finite reference maximum (exp2_fma2 gives
+                // once every row has a finite reference maximum (exp2_fma2_quartic gives
                 // 2^-126 for a masked score, nothing next to l >= 1)
                 float2 lsum = make_float2(0.f, 0.f), lsum2 = make_float2(0.f, 0.f);
                 const float2 neg_m2 = make_float2(-m_use, -m_use);
@@ -521,7 +521,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         const float2 a = __ffma2_rn(make_float2(x[c], x[c + 1]), qk2, neg_m2);
                         float2 pp;
                         if (kEmu && c2 % kEmuEvery == kEmuEvery - 1)
-                            pp = exp2_fma2(a);
+                            pp = exp2_fma2_quartic(a);
                         else
                             pp = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                         if (c2 & 1)
@@ -599,7 +599,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             };
             auto store_lse = [&](float m, float sum) {
                 if (!valid) return;
-                const float lse2 = sum > 0.f ? m + lg2_approx(sum) : neg_inf();
+                const float lse2 = sum == 0.f ? neg_inf() : m + lg2_approx(sum);
                 if (s.dest < 0)
                     p.lse[static_cast<long long>(head) * p.T + t] = lse2 * kLn2;
                 else
@@ -610,7 +610,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 tc_fence_after();
                 if (active) {
-                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                     for (int cc = 0; cc < D / 32; ++cc) {
                         uint32_t r[32];
@@ -638,7 +638,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     const float a = m_ref == neg_inf() ? 0.f : ex2_approx(m_ref - m);
                     const float b = other.x == neg_inf() ? 0.f : ex2_approx(other.x - m);
                     const float sum = l * a + other.y * b;
-                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     const float w_own = a * inv, w_oth = b * inv;
 #pragma unroll
                     for (int cc = 0; cc < D / 64; ++cc) {
@@ -676,7 +676,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 // unit (its partial result 1), CTAs c + 1 .. last continue it (their partial
 // results 0); added in that order.  One warp per row.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedFwdParams p) {
+__global__ void __launch_bounds__(256, 6) fa_paged_merge_kernel(const __grid_constant__ PagedFwdParams p) {
     constexpr int kPer = D / 32;
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int ur = blockIdx.y * 8 + (threadIdx.x >> 5);
@@ -687,22 +687,30 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
         return static_cast<size_t>(i == c ? 2 * c + 1 : 2 * i) * p.part_rows + ur;
     };
     float m = neg_inf();
-    for (int i = c + lane; i <= mm.last; i += 32) m = fmaxf(m, p.lse_part[index(i)]);
+    bool nan = false;                   // of a row of NaN: it stays one
+    for (int i = c + lane; i <= mm.last; i += 32) {
+        const float x = p.lse_part[index(i)];
+        nan |= x != x;
+        m = fmaxf(m, x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float acc[kPer], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    if (__any_sync(0xffffffffu, nan)) m = 0.f;
     if (m != neg_inf()) {
         for (int i0 = c; i0 <= mm.last; i0 += 32) {
-            // lane k has the weight of part i0 + k; the parts' rows kU at a time
-            constexpr int kU = 8;
+            // lane k has the weight of part i0 + k
             const int cnt = min(32, mm.last + 1 - i0);
             const float wl = lane < cnt ? ex2_approx(p.lse_part[index(i0 + lane)] - m) : 0.f;     // -inf: 0
-            for (int k = 0; k < cnt; k += kU) {
-                float w[kU], v[kU][kPer];
+            // the parts' rows, U loads in flight (more cost the occupancy that many
+            // rows of two parts need)
+            auto add = [&](auto n, int k) {
+                constexpr int U = decltype(n)::value;
+                float w[U], v[U][kPer];
 #pragma unroll
-                for (int q = 0; q < kU; ++q) {
+                for (int q = 0; q < U; ++q) {
                     w[q] = __shfl_sync(0xffffffffu, wl, (k + q) & 31);
                     const float *src = p.o_part + index(i0 + min(k + q, cnt - 1)) * D + lane * kPer;
                     if constexpr (kPer == 4) {
@@ -714,22 +722,25 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < kU; ++q) {
+                for (int q = 0; q < U; ++q) {
                     if (k + q >= cnt) break;
                     sum += w[q];
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w[q], v[q][e], acc[e]);
                 }
-            }
+            };
+            int k = 0;
+            for (; k + 2 < cnt; k += 4) add(std::integral_constant<int, 4>{}, k);
+            for (; k < cnt; k += 2) add(std::integral_constant<int, 2>{}, k);
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int t = mm.row0 + ur / p.G, head = mm.h * p.G + ur % p.G;
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + head * p.o_h + t * p.o_n + lane * kPer);
 #pragma unroll
     for (int e = 0; e < kPer / 2; ++e) dst[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     if (lane == 0)
-        p.lse[static_cast<long long>(head) * p.T + t] = sum > 0.f ? (m + lg2_approx(sum)) * kLn2 : neg_inf();
+        p.lse[static_cast<long long>(head) * p.T + t] = sum == 0.f ? neg_inf() : (m + lg2_approx(sum)) * kLn2;
 }
 
 template <int D, bool BF16>

@@ -534,10 +534,10 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             if (named_bar_or(wg_bar, 128, !done)) { ok = false; break; }
             if (key < rows) {
                 const float sum = (red[key] + red[C + key]) + (red[2 * C + key] + red[3 * C + key]);
-                const float lse2 = sum > 0.f ? m_ref[key] + lg2_approx(sum) : neg_inf();
+                const float lse2 = sum == 0.f ? neg_inf() : m_ref[key] + lg2_approx(sum);
                 const int r = row0 + key, tok = r / p.G, head = s.h * p.G + r - tok * p.G;
                 const size_t part = (2 * blockIdx.x + s.dest) * static_cast<size_t>(p.part_rows) + r;
-                row_state[key].factor = sum > 0.f ? 1.f / sum : 0.f;
+                row_state[key].factor = sum == 0.f ? 0.f : 1.f / sum;
                 row_state[key].at = s.dest < 0 ? head * p.o_h + (s.row0 + tok) * p.o_n : static_cast<long long>(part) * D;
                 if (s.dest < 0)
                     p.lse[static_cast<long long>(head) * p.T + s.row0 + tok] = lse2 * kLn2;
