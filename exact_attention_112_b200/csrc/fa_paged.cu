@@ -198,7 +198,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (w.n == 0) {
                         write_empty<D>(p, s.row0, s.ntok, s.h, lane);
                     } else if (!w.none()) {
-                        if (w.t0 == 0 && w.t1 < w.n) mm = MergeMeta{s.row0, s.ntok, s.h, w.last_cta(pc)};
+                        if (w.t0 == 0 && w.t1 < w.n) mm = MergeMeta{s.row0, s.ntok, s.h, w.last_cta(pc, p.geom)};
                         ok = push(s);
                     }
                 } while (ok && w.next(p, p.geom));

@@ -132,10 +132,18 @@ fa::SchedGeom sched_geom(int G, int max_q) {
     fa::SchedGeom g;
     g.tile_tokens = std::max(1, std::min(128 / G, max_q));
     g.unit_tokens = std::max(1, std::min(2 * (128 / G), max_q));
-    if (max_q * G <= fa::kPagedTokenRows) g.tile_tokens = g.unit_tokens;    // one unit per sequence and kv head
-    // a key tile of one row tile takes 1.44 us, of two 2.03
-    g.one_cost = g.unit_tokens > g.tile_tokens ? 5 : 1;
-    g.two_cost = 7;
+    // Costs, measured: single tokens take 1.5 us a key tile (the memory's rate) and
+    // 2 us a unit; in the kernel of row tiles a key tile takes 1.44 us with one,
+    // 2.03 us with two of them, a unit 3 us.
+    if (max_q * G <= fa::kPagedTokenRows) {
+        g.tile_tokens = g.unit_tokens;      // one unit per sequence and kv head
+        g.unit_cost = 3;
+        g.one_cost = g.two_cost = 2;
+    } else {
+        g.unit_cost = 10;
+        g.one_cost = 5;
+        g.two_cost = 7;
+    }
     return g;
 }
 
@@ -296,10 +304,9 @@ int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_stride
     p.geom = sched_geom(G, p.max_q);
     p.part_rows = p.geom.unit_tokens * G;
     const bool tokens = p.part_rows <= fa::kPagedTokenRows;
-    // the tile kernel works on two key tiles at a time; every piece holds the
-    // first entry of a key tile (two_cost <= min_piece / 2)
-    p.min_piece = tokens ? 1 : p.geom.one_cost > 1 ? 14 : 2;
-    p.o_v8 = aligned(o, 32) && p.o_h % 16 == 0 && p.o_n % 16 == 0;
+    // a key tile at least; two for the kernel of row tiles, which works on two at
+    // a time (half a piece holds the first entry of some key tile)
+    p.min_piece = tokens ? 2 : 14;
     const PagedWorkspace w = paged_workspace(p.geom, G, D);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.o_part = reinterpret_cast<float *>(ws);

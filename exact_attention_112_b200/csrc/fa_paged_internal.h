@@ -88,7 +88,8 @@ constexpr int kPagedTile = 128;         // keys per tile
 struct SchedGeom {
     int unit_tokens;    // tokens per unit
     int tile_tokens;    // tokens per tile of query rows (a unit past it has two)
-    int one_cost, two_cost;     // entries that a key tile of a unit of one or two row tiles counts
+    int unit_cost;              // entries that a unit counts by itself,
+    int one_cost, two_cost;     // and each of its key tiles, with one or two row tiles
 };
 
 // What the merge kernel reads of CTA c: the unit that c begins and does not

@@ -12,9 +12,10 @@
 // which a second kernel merges in the order of the CTAs, so the result does not
 // depend on timing.
 //
-// A key tile of a unit counts `one_cost` entries, or `two_cost` where the unit
-// has two tiles of query rows: about what the two take.  A unit without a
-// visible key counts as one tile: its rows have to be written.
+// A unit counts `unit_cost` entries, for what its beginning and end take, and then
+// for each of its key tiles `one_cost`, or `two_cost` where it has two tiles of
+// query rows.  A unit without a visible key counts as one tile: its rows have to
+// be written.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,7 +38,7 @@ __device__ __forceinline__ int unit_tiles(const PagedSeq &s, int tok0, const Sch
 
 __device__ __forceinline__ long long unit_cost(const PagedSeq &s, int tok0, const SchedGeom &g, int causal) {
     const long long n = max(1, unit_tiles(s, tok0, g, causal));
-    return n * (tok0 + g.tile_tokens < s.new_q ? g.two_cost : g.one_cost);
+    return g.unit_cost + n * (tok0 + g.tile_tokens < s.new_q ? g.two_cost : g.one_cost);
 }
 
 // Work of one kv head of each lane's sequence.  A sequence of many units is
@@ -188,7 +189,7 @@ struct SegWalk {
         n = unit_tiles(s, tok0, g, p.causal);
         two = tok0 + g.tile_tokens < s.new_q;
         w = two ? g.two_cost : g.one_cost;
-        cost = static_cast<long long>(w) * max(1, n);
+        cost = g.unit_cost + static_cast<long long>(w) * max(1, n);
     }
 
     // By a whole warp: the unit that holds entry lo.
@@ -222,14 +223,14 @@ struct SegWalk {
             base += __shfl_sync(0xffffffffu, inc, 31);
         }
         unit(p, g);
-        range();
+        range(g);
     }
 
-    // Key tile j is the CTA's that holds the unit's entry w * j.
-    __device__ __forceinline__ void range() {
-        const long long a = lo - base, z = hi - base;
+    // Key tile j is the CTA's that holds the unit's entry unit_cost + w * j.
+    __device__ __forceinline__ void range(const SchedGeom &g) {
+        const long long a = lo - base - g.unit_cost, z = hi - base - g.unit_cost;
         t0 = a <= 0 ? 0 : static_cast<int>(min(static_cast<long long>(n), div_wide(a + w - 1, w)));
-        t1 = z >= cost ? n : static_cast<int>(min(static_cast<long long>(n), div_wide(z + w - 1, w)));
+        t1 = z <= 0 ? 0 : base + cost <= hi ? n : static_cast<int>(min(static_cast<long long>(n), div_wide(z + w - 1, w)));
     }
 
     // The next unit of the piece; false when there is none.
@@ -248,19 +249,19 @@ struct SegWalk {
             }
         }
         unit(p, g);
-        range();
+        range(g);
         return true;
     }
 
     // Does this segment write the unit's rows itself?
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
 
-    // Nothing of the unit falls to this CTA (a boundary inside a doubled entry).
+    // Nothing of the unit falls to this CTA (a boundary inside its beginning, or a tile's entries).
     __device__ __forceinline__ bool none() const { return n > 0 && t0 >= t1; }
 
     // CTA that holds the unit's last key tile.
-    __device__ __forceinline__ int last_cta(const Piece &pc) const {
-        const long long at = base + static_cast<long long>(w) * (n - 1), wide = pc.rem * (pc.quot + 1);
+    __device__ __forceinline__ int last_cta(const Piece &pc, const SchedGeom &g) const {
+        const long long at = base + g.unit_cost + static_cast<long long>(w) * (n - 1), wide = pc.rem * (pc.quot + 1);
         return static_cast<int>(at < wide ? div_wide(at, pc.quot + 1) : pc.rem + div_wide(at - wide, pc.quot));
     }
 };
