@@ -38,7 +38,7 @@
 #include "fa_internal.h"
 #include "fa_paged_internal.h"
 #include "fa_paged_sched.cuh"
-#include "fa_ptx.cuh"
+#include "fa_paged_ptx.cuh"
 
 namespace fa {
 namespace {

@@ -22,7 +22,7 @@
 #include <cuda_fp16.h>
 
 #include "fa_paged_internal.h"
-#include "fa_ptx.cuh"
+#include "fa_paged_ptx.cuh"
 
 namespace fa {
 

@@ -5,7 +5,7 @@ import re
 
 import numpy as np
 
-HDR = os.path.join(os.path.dirname(__file__), "..", "exact_attention_112_b200", "csrc", "fa_ptx.cuh")
+HDR = os.path.join(os.path.dirname(__file__), "..", "exact_attention_112_b200", "csrc", "fa_paged_ptx.cuh")
 
 
 def _fma(a, b, c):
