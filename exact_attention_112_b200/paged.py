@@ -197,16 +197,20 @@ def _rows(what, name, t, shape, dtype, device, low=0):
         _bad(what, f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         _bad(what, f"{name} must be on {device}, got {t.device}")
-    st = t.stride()
-    if st[-1] != 1:
-        _bad(what, f"{name} rows must be contiguous")
-    for n, s in zip(shape, st[:-1]):
-        if (s & 7 or s < low) and n > 1:
-            _bad(what, f"{name} strides must be multiples of 8" + (" and at least D" if low else ""))
-    ptr = t.data_ptr()
-    if ptr & 15:
-        _bad(what, f"{name} must start 16-byte aligned")
+    st, ptr = t.stride(), t.data_ptr()
+    # the two innermost first: heads and rows, all that a packed tensor has
+    if st[-1] != 1 or (st[-2] | st[-3]) & 7 or st[-2] < low or st[-3] < low or len(st) > 3 or ptr & 15:
+        if st[-1] != 1:
+            _bad(what, f"{name} rows must be contiguous")
+        for n, s in zip(shape, st[:-1]):
+            if (s & 7 or s < low) and n > 1:
+                _bad(what, f"{name} strides must be multiples of 8" + (" and at least D" if low else ""))
+        if ptr & 15:
+            _bad(what, f"{name} must start 16-byte aligned")
     return ptr, st
+
+
+_AS_IT_IS = contextlib.nullcontext()
 
 
 def _allocating_on(stream):
@@ -214,7 +218,7 @@ def _allocating_on(stream):
     memory that a kernel of another stream fills must not come from, nor go back
     to, the pool of the current one."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _AS_IT_IS
     import torch
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
@@ -226,25 +230,26 @@ def _need_rope(what, rope):
 
 def _positions(what, positions, B, N, device):
     """(pointer, stride between batches) of int32 positions [B, N], or [N] for every batch."""
-    import torch
     if positions is None:
         return None, 0
-    if positions.dtype != torch.int32:
+    import torch
+    if positions.dtype is not torch.int32:
         _bad(what, f"positions must be torch.int32, got {positions.dtype}")
-    shape = tuple(positions.shape)
-    if shape not in ((B, N), (N,)):
-        _bad(what, f"positions must have shape {(B, N)} or {(N,)}, got {shape}")
-    if N > 1 and positions.stride(-1) != 1:
+    shape, st = positions.shape, positions.stride()
+    if shape != (B, N) and shape != (N,):
+        _bad(what, f"positions must have shape {(B, N)} or {(N,)}, got {tuple(shape)}")
+    if st[-1] != 1 and N > 1:
         _bad(what, "positions must be contiguous along the rows")
     if positions.device != device:
         _bad(what, f"positions must be on {device}, got {positions.device}")
-    bstride = positions.stride(0) if len(shape) == 2 and B > 1 else 0
+    bstride = st[0] if len(st) == 2 and B > 1 else 0
     if bstride < 0:
         _bad(what, "positions must not have negative strides")
     return positions.data_ptr(), bstride
 
 
-def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream):
+def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream, fresh=False):
+    """fresh: the outputs come from empty_like, so they are as they have to be."""
     if q is None or q.dim() not in (3, 4):
         _bad(what, "q must be [B, H, N, D] or [H, total, D]")
     code = _dtype_code(q)
@@ -263,7 +268,7 @@ def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream):
         _bad(what, f"rope must be on {q.device}, got {rope.device}")
     dtype, device = q.dtype, q.device
     qp, qs = _rows(what, "q", q, shape, dtype, device)
-    qop, qos = _rows(what, "q_out", q_out, shape, dtype, device, D)
+    qop, qos = (q_out.data_ptr(), q_out.stride()) if fresh else _rows(what, "q_out", q_out, shape, dtype, device, D)
     Hk, kp, kop, ks, kos = 0, None, None, None, None
     if k is not None:
         if k.dim() != len(shape):
@@ -271,7 +276,7 @@ def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream):
         Hk = k.shape[-3]
         kshape = (*shape[:-3], Hk, N, D)
         kp, ks = _rows(what, "k", k, kshape, dtype, device)
-        kop, kos = _rows(what, "k_out", k_out, kshape, dtype, device, D)
+        kop, kos = (k_out.data_ptr(), k_out.stride()) if fresh else _rows(what, "k_out", k_out, kshape, dtype, device, D)
         if Hk == 0:
             kp = kop = ks = kos = None
     elif k_out is not None:
@@ -304,7 +309,7 @@ def rope_forward(q, k, rope, positions=None, offset=0, stream=None):
     with _allocating_on(stream):
         q_out = torch.empty_like(q)
         k_out = None if k is None else torch.empty_like(k)
-    fa_rope(q, k, q_out, k_out, rope, positions=positions, offset=offset, stream=stream)
+    _rope_call("fa_rope", q, k, q_out, k_out, rope, positions, offset, stream, fresh=True)
     return q_out, k_out
 
 
@@ -314,7 +319,7 @@ def rope_backward(dq_out, dk_out, rope, positions=None, offset=0, stream=None):
     with _allocating_on(stream):
         dq = torch.empty_like(dq_out)
         dk = None if dk_out is None else torch.empty_like(dk_out)
-    fa_rope_bwd(dq_out, dk_out, dq, dk, rope, positions=positions, offset=offset, stream=stream)
+    _rope_call("fa_rope_bwd", dq_out, dk_out, dq, dk, rope, positions, offset, stream, fresh=True)
     return dq, dk
 
 
