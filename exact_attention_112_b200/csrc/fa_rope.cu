@@ -115,7 +115,7 @@ __device__ __forceinline__ void unit_offsets(int u, int rot, int D, int &o0, int
 }
 
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p, int heads_per_group) {
+__global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const RopeParams p, int heads_per_group) {
     const int units = (p.D + 15) / 16;
     const long long tokens = static_cast<long long>(p.B) * p.N;
     const long long idx = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -126,35 +126,42 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     int o0, o1;
     bool turn;
     unit_offsets<INTER>(u, p.rot, p.D, o0, o1, turn);
-    Angles an;
-    if (turn) {
-        const int pos = p.positions ? __ldg(p.positions + b * p.pos_stride + n) : p.pos0 + n;
-        an.set(p.inv_freq + 8 * u, pos, p.scale, p.sign);
-    }
     const int all = p.q.H + p.k.H;
     const int h_end = min(static_cast<int>(blockIdx.y + 1) * heads_per_group, all);
-    for (int h0 = blockIdx.y * heads_per_group; h0 < h_end; h0 += 4) {
-        uint4 x[4], y[4];
-        const uint16_t *src[4];
-        uint16_t *dst[4];
+    int h0 = blockIdx.y * heads_per_group;
+    uint4 x[4], y[4];
+    auto load = [&]() {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int h = min(h0 + j, h_end - 1);
             const bool isq = h < p.q.H;
             const RopeTensor &t = isq ? p.q : p.k;
-            const int hh = isq ? h : h - p.q.H;
-            src[j] = static_cast<const uint16_t *>(t.in) + b * t.in_b + hh * t.in_h + n * t.in_n;
-            dst[j] = static_cast<uint16_t *>(t.out) + b * t.out_b + hh * t.out_h + n * t.out_n;
-            x[j] = *reinterpret_cast<const uint4 *>(src[j] + o0);
-            if (o1 >= 0) y[j] = *reinterpret_cast<const uint4 *>(src[j] + o1);
+            const uint16_t *src = static_cast<const uint16_t *>(t.in) + b * t.in_b + (isq ? h : h - p.q.H) * t.in_h + n * t.in_n;
+            x[j] = *reinterpret_cast<const uint4 *>(src + o0);
+            if (o1 >= 0) y[j] = *reinterpret_cast<const uint4 *>(src + o1);
         }
+    };
+    load();     // on their way while the angles are computed
+    Angles an;
+    if (turn) {
+        const int pos = p.positions ? __ldg(p.positions + b * p.pos_stride + n) : p.pos0 + n;
+        an.set(p.inv_freq + 8 * u, pos, p.scale, p.sign);
+    }
+    for (;;) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (h0 + j >= h_end) break;
+            const int h = h0 + j;
+            if (h >= h_end) break;
+            const bool isq = h < p.q.H;
+            const RopeTensor &t = isq ? p.q : p.k;
+            uint16_t *dst = static_cast<uint16_t *>(t.out) + b * t.out_b + (isq ? h : h - p.q.H) * t.out_h + n * t.out_n;
             if (turn) rotate<BF16, INTER>(x[j], y[j], an);
-            *reinterpret_cast<uint4 *>(dst[j] + o0) = x[j];
-            if (o1 >= 0) *reinterpret_cast<uint4 *>(dst[j] + o1) = y[j];
+            *reinterpret_cast<uint4 *>(dst + o0) = x[j];
+            if (o1 >= 0) *reinterpret_cast<uint4 *>(dst + o1) = y[j];
         }
+        h0 += 4;
+        if (h0 >= h_end) break;
+        load();
     }
 }
 
@@ -163,20 +170,45 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
 // H + 2 Hkv rows of that token.  Tokens of no sequence, and positions whose
 // page the table does not give, are left alone.
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) fa_paged_append_kernel(const AppendParams p, int heads_per_group) {
+__global__ void __launch_bounds__(kRopeThreads, 3) fa_paged_append_kernel(const AppendParams p, int heads_per_group) {
     const int D = p.kv.D;
     const int units = D / 16;
     const int per_block = kRopeThreads / units;
-    // the sequence of the block's first token: how many sequences end at or before it
     const int t0 = blockIdx.x * per_block;
+    const int lt = threadIdx.x / units, u = threadIdx.x - lt * units;
+    const int t = t0 + lt;
+    const bool live = lt < per_block && t < p.T;
+    int o0, o1;
+    bool turn;
+    unit_offsets<INTER>(u, p.rot, D, o0, o1, turn);
+    const int all = p.H + 2 * p.kv.Hkv;
+    const int h_end = min(static_cast<int>(blockIdx.y + 1) * heads_per_group, all);
+    int h0 = blockIdx.y * heads_per_group;
+    uint4 x[4], y[4];
+    auto load = [&]() {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int h = min(h0 + j, h_end - 1);
+            const uint16_t *src;
+            if (h < p.H)
+                src = static_cast<const uint16_t *>(p.q) + h * p.q_h + t * p.q_n;
+            else if (h < p.H + p.kv.Hkv)
+                src = static_cast<const uint16_t *>(p.k) + (h - p.H) * p.k_h + t * p.k_n;
+            else
+                src = static_cast<const uint16_t *>(p.v) + (h - p.H - p.kv.Hkv) * p.v_h + t * p.v_n;
+            x[j] = *reinterpret_cast<const uint4 *>(src + o0);
+            y[j] = *reinterpret_cast<const uint4 *>(src + o1);
+        }
+    };
+    // the first rows are on their way while the tables are searched
+    if (live) load();
+    // the sequence of the block's first token: how many sequences end at or before it
     int b = 0;
     for (int i = 0; i < p.kv.num_seqs; i += kRopeThreads) {
         const int s = i + threadIdx.x;
         b += __syncthreads_count(s < p.kv.num_seqs && __ldg(p.cu + s + 1) <= t0);
     }
-    const int lt = threadIdx.x / units, u = threadIdx.x - lt * units;
-    const int t = t0 + lt;
-    if (lt >= per_block || t >= p.T) return;
+    if (!live) return;
     while (b < p.kv.num_seqs && __ldg(p.cu + b + 1) <= t) ++b;
     if (b >= p.kv.num_seqs) return;
     const int first = __ldg(p.cu + b), end = __ldg(p.cu + b + 1);
@@ -191,52 +223,36 @@ __global__ void __launch_bounds__(kRopeThreads) fa_paged_append_kernel(const App
         page = __ldg(p.kv.table + b * p.kv.table_stride + pi);
         if (page >= p.kv.num_pages) page = -1;
     }
-    int o0, o1;
-    bool turn;
-    unit_offsets<INTER>(u, p.rot, D, o0, o1, turn);
     Angles an;
     if (turn) {
         const int pos = p.positions ? __ldg(p.positions + t) : static_cast<int>(at);
         an.set(p.inv_freq + 8 * u, pos, p.scale, 1.f);
     }
-    const int all = p.H + 2 * p.kv.Hkv;
-    const int h_end = min(static_cast<int>(blockIdx.y + 1) * heads_per_group, all);
-    for (int h0 = blockIdx.y * heads_per_group; h0 < h_end; h0 += 4) {
-        uint4 x[4], y[4];
-        uint16_t *dst[4];
-        bool rot[4];
+    for (;;) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int h = min(h0 + j, h_end - 1);
-            const uint16_t *src;
+            const int h = h0 + j;
+            if (h >= h_end) break;
+            uint16_t *dst;
+            bool rot = turn;
             if (h < p.H) {
-                src = static_cast<const uint16_t *>(p.q) + h * p.q_h + t * p.q_n;
-                dst[j] = static_cast<uint16_t *>(p.q_out) + h * p.qo_h + t * p.qo_n;
-                rot[j] = turn;
+                dst = static_cast<uint16_t *>(p.q_out) + h * p.qo_h + t * p.qo_n;
+            } else if (page < 0) {
+                continue;
             } else if (h < p.H + p.kv.Hkv) {
-                const int hk = h - p.H;
-                src = static_cast<const uint16_t *>(p.k) + hk * p.k_h + t * p.k_n;
-                dst[j] = page < 0 ? nullptr
-                                  : static_cast<uint16_t *>(p.kv.k) + page * p.kv.k_page + hk * p.kv.k_head + row * p.kv.k_tok;
-                rot[j] = turn;
+                dst = static_cast<uint16_t *>(p.kv.k) + page * p.kv.k_page + (h - p.H) * p.kv.k_head + row * p.kv.k_tok;
             } else {
-                const int hk = h - p.H - p.kv.Hkv;
-                src = static_cast<const uint16_t *>(p.v) + hk * p.v_h + t * p.v_n;
-                dst[j] = page < 0 ? nullptr
-                                  : static_cast<uint16_t *>(p.kv.v) + page * p.kv.v_page + hk * p.kv.v_head + row * p.kv.v_tok;
-                rot[j] = false;
+                dst = static_cast<uint16_t *>(p.kv.v) + page * p.kv.v_page + (h - p.H - p.kv.Hkv) * p.kv.v_head +
+                      row * p.kv.v_tok;
+                rot = false;
             }
-            x[j] = *reinterpret_cast<const uint4 *>(src + o0);
-            y[j] = *reinterpret_cast<const uint4 *>(src + o1);
+            if (rot) rotate<BF16, INTER>(x[j], y[j], an);
+            *reinterpret_cast<uint4 *>(dst + o0) = x[j];
+            *reinterpret_cast<uint4 *>(dst + o1) = y[j];
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (h0 + j >= h_end) break;
-            if (dst[j] == nullptr) continue;
-            if (rot[j]) rotate<BF16, INTER>(x[j], y[j], an);
-            *reinterpret_cast<uint4 *>(dst[j] + o0) = x[j];
-            *reinterpret_cast<uint4 *>(dst[j] + o1) = y[j];
-        }
+        h0 += 4;
+        if (h0 >= h_end) break;
+        load();
     }
 }
 

@@ -350,7 +350,7 @@ typedef struct fa_paged_kv {
  *   q, q_out   optional (both NULL with Hq = 0): [Hq, total_q, D] queries of the
  *              same rows, rotated in the same launch (in place allowed).
  *              Needs a rope.
- * Rows of no sequence are neither read nor written.  Sequences must not share
+ * Rows of no sequence are not written.  Sequences must not share
  * the pages that they write.
  */
 int fa_paged_append(const fa_paged_kv *kv, const void *k, const long long *k_strides, const void *v,
