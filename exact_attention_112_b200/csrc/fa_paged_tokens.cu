@@ -17,6 +17,12 @@
 // more than 2^8, which one vote over the warpgroup finds out; the row sums stay
 // spread over the threads until the unit's end.
 //
+// Measured (D = 128, G = 4): 64 tokens over 512..8192 keys in pages of 16, 1143
+// MB, 185 us, 6.16 TB/s; one token over 65536 keys, 8 heads, 55.9 us (41 at the
+// copy rate); one over 1000 keys 7 us and 2.5 of merging.  With row tiles of 128
+// for those rows (fa_paged.cu) the first took 255 us: the softmax of one tile
+// held its V for longer than the ring covers.
+//
 // Warps: one warpgroup of softmax (two for R = 64, half of the rows each), then a
 // TMA warp (each lane looks up the page of its box), an MMA warp, and one that
 // walks the CTA's share of the work (fa_paged_sched.cuh).

