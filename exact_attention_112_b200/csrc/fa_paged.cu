@@ -125,8 +125,11 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
+    // This grid may have been started while the one before it in the stream still
+    // ran: nothing is read or written before that has ended.
+    grid_dependency_wait();
     PlanSeqs seqs;
-    if (warp == kPlanWarp) plan_load(p, 0, lane, seqs);    // the tables arrive during the set-up
+    if (warp == kPlanWarp) plan_load(p, 0, lane, seqs);     // the tables arrive during the set-up
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
         tmem_relinquish();
@@ -296,7 +299,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const uint64_t dk = KT::k_desc(sbase + L::kK + st * L::kTileBytes);
             const uint32_t d = tmem + L::kColS + slot * 128;
             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
                     umma_f16_ss(d, dq + off, dk + KT::k_step(kk), idesc_qk, kk > 0);
@@ -365,41 +368,44 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         ok = enter(cs);
         cp = cs;
         for (int i = 0; i < 2 && ok; ++i) ok = step_s();
-        // PV(q), S(q + 2) for every job q; the S of the segment's own later
-        // tiles without step_s's bookkeeping (a wait that is not needed costs the
-        // MMA warp some 300 cycles of a 1700-cycle job)
+        // PV(q), S(q + 2) for every job q.  The MMA warp paces the kernel, and what it
+        // costs is instructions fetched past those of eight softmax warps: the loop
+        // over a segment's tiles is kept free of what only its last tile needs, its
+        // waits for K and V stand where it waits for P anyway, and the products of S
+        // are rolled by two (2 x 2048 tokens over 16384 keys: 807 us with one general
+        // loop and a second variant of the softmax, 739 so; rolled by four 749,
+        // unrolled 748, P V rolled too 770).
         while (ok && cp.jobs > 0) {
             if (cp.two) {
                 const int nt = cp.jobs >> 1, sa = cp.g & 1, sb = sa ^ 1;
                 const int qa = (cs.u == cp.u ? q_n : 0) & 1, qb = qa ^ 1;     // used while S of this segment are left
-                for (int j = 0; j < nt; ++j) {
-                    const bool last = j + 1 == nt;
+                for (int j = 0; j + 1 < nt; ++j) {
                     const int st = cp.t % kStages, st1 = (cp.t + 1) % kStages;
-                    if (!(ok = wait_v(cp.t, last ? cp.tail : kBN))) break;
-                    if (!(ok = issue_pv(sa, (cp.g >> 1) & 1, st, j > 0, false, last))) break;
-                    if (!last) {
-                        if (!(ok = wait_k(cp.t + 1))) break;
-                        tc_fence_after();
-                        issue_s(sa, qa, st1, false, j + 2 == nt);
-                    } else if (!(ok = step_s())) {
-                        break;
-                    }
-                    if (!(ok = issue_pv(sb, ((cp.g + 1) >> 1) & 1, st, j > 0, true, last))) break;
-                    if (!last) {
-                        issue_s(sb, qb, st1, true, j + 2 == nt);
-                        if (j + 2 == nt) {
-                            cs.g = cp.g + 4;
-                            cs.t = cp.t + 2;
-                            q_n += 2;
-                            ++cs.u;
-                            if (!(ok = enter(cs))) break;
-                        }
-                    } else if (!(ok = step_s())) {
-                        break;
-                    }
+                    const bool ends = j + 2 == nt;          // S of the segment's last tile
+                    if (!(ok = wait_v(cp.t, kBN) && wait_k(cp.t + 1))) break;
+                    if (!(ok = issue_pv(sa, (cp.g >> 1) & 1, st, j > 0, false, false))) break;
+                    issue_s(sa, qa, st1, false, ends);
+                    if (!(ok = issue_pv(sb, ((cp.g + 1) >> 1) & 1, st, j > 0, true, false))) break;
+                    issue_s(sb, qb, st1, true, ends);
                     cp.g += 2;
                     ++cp.t;
                 }
+                if (!ok) break;
+                if (nt > 1) {
+                    cs.g = cp.g + 2;
+                    cs.t = cp.t + 1;
+                    q_n += 2;
+                    ++cs.u;
+                    if (!(ok = enter(cs))) break;
+                }
+                const int st = cp.t % kStages;
+                if (!(ok = wait_v(cp.t, cp.tail))) break;
+                if (!(ok = issue_pv(sa, (cp.g >> 1) & 1, st, nt > 1, false, true))) break;
+                if (!(ok = step_s())) break;
+                if (!(ok = issue_pv(sb, ((cp.g + 1) >> 1) & 1, st, nt > 1, true, true))) break;
+                if (!(ok = step_s())) break;
+                cp.g += 2;
+                ++cp.t;
             } else {
                 for (int j = 0; j < cp.jobs; ++j) {
                     if (!(ok = wait_v(cp.t, j + 1 == cp.jobs ? cp.tail : kBN))) break;
@@ -511,22 +517,21 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 const float m_use = (m_ref == neg_inf()) ? 0.f : m_ref;
                 // p = 2^(x - m) in two halves of 64 keys, each handed to the MMA
-                // warp on its own barrier; one pair in kEmuEvery on the FMA pipe
-                // once every row has a finite reference maximum (exp2_fma2_quartic gives
-                // 2^-126 for a masked score, nothing next to l >= 1)
+                // warp on its own barrier; one pair in kEmuEvery on the FMA pipe, where
+                // exp2_fma2_quartic gives 2^-126 for a masked score: nothing next to
+                // l >= 1, and a row that has seen no key yet is cleared when it sees
+                // one (alpha = 0) or at the end
                 float2 lsum = make_float2(0.f, 0.f), lsum2 = make_float2(0.f, 0.f);
                 const float2 neg_m2 = make_float2(-m_use, -m_use);
                 const float2 qk2 = make_float2(qk, qk);
-                const bool emu = __all_sync(0xffffffffu, m_ref != neg_inf());
-                auto half = [&](int h, auto emu_tag) {
-                    constexpr bool kEmu = decltype(emu_tag)::value;
+                auto half = [&](int h) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int c2 = 0; c2 < 32; ++c2) {
                         const int c = 64 * h + 2 * c2;
                         const float2 a = __ffma2_rn(make_float2(x[c], x[c + 1]), qk2, neg_m2);
                         float2 pp;
-                        if (kEmu && c2 % kEmuEvery == kEmuEvery - 1)
+                        if (c2 % kEmuEvery == kEmuEvery - 1)
                             pp = exp2_fma2_quartic(a);
                         else
                             pp = make_float2(ex2_approx(a.x), ex2_approx(a.y));
@@ -538,15 +543,12 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
                     tmem_st32dp_x32(tS + 32 * h, pk);
                 };
-                if (emu)
-                    half(0, std::true_type{});
-                else
-                    half(0, std::false_type{});
+                half(0);
                 if (rescale && later) {
                     // O row *= alpha.  O is stable: this S tile's MMA was issued
                     // after the slot's previous P V and its commit covers it.
                     const uint32_t tO = tl + L::kColO + slot * D;
-#pragma unroll
+#pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
                         uint32_t orr[32];
                         tmem_ld32dp_x32_wait(tO + cc * 32, orr);
@@ -558,10 +560,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(L::kPHalf + 2 * slot));
-                if (emu)
-                    half(1, std::true_type{});
-                else
-                    half(1, std::false_type{});
+                half(1);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(L::kPHalf + 2 * slot + 1));
@@ -570,6 +569,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
 
             // ---- the rows' results: O = o / l, LSE = (m_ref + log2 l) ln 2
+            if (m_ref == neg_inf() && l == l) l = 0.f;      // no key was seen (a row of NaN stays NaN)
             const int r_tok = row / p.G, r_head = row - r_tok * p.G;
             const int tok = (s.two ? first * p.geom.tile_tokens : 0) + r_tok;
             const bool valid = r_tok < p.geom.tile_tokens && tok < s.ntok;
@@ -686,6 +686,7 @@ __global__ void __launch_bounds__(256, 6) fa_paged_merge_kernel(const __grid_con
     constexpr int kPer = D / 32;
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int ur = blockIdx.y * 8 + (threadIdx.x >> 5);
+    grid_launch_dependents();           // the next call may be set up; it waits for this grid
     grid_dependency_wait();             // the partial results are complete and visible
     const MergeMeta mm = p.meta[c];
     if (mm.last < 0 || ur >= mm.tokens * p.G) return;
@@ -755,29 +756,21 @@ cudaError_t launch_t(const PagedTensorMaps &tm, const PagedFwdParams &p, int gri
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PagedLayout<D>::kAlloc);
     if (e != cudaSuccess) return e;
     prof_begin(stream, "fa_paged_kernel");
-    kern<<<grid, kThreads, PagedLayout<D>::kAlloc, stream>>>(tm.q, tm.k, tm.v, p);
+    e = launch_early(kern, dim3(grid), kThreads, PagedLayout<D>::kAlloc, stream, tm.q, tm.k, tm.v, p);
     prof_end(stream);
     note_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     return launch_paged_merge(p, BF16, grid, stream);
 }
 
 template <int D, bool BF16>
 cudaError_t launch_merge_t(const PagedFwdParams &p, int grid, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, (p.part_rows + 7) / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     prof_begin(stream, "fa_paged_merge_kernel");
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, BF16>, p);
+    const cudaError_t e =
+        launch_early(fa_paged_merge_kernel<D, BF16>, dim3(grid, (p.part_rows + 7) / 8), 256, 0, stream, p);
     prof_end(stream);
     note_launch();
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return e;
 }
 
 }  // namespace

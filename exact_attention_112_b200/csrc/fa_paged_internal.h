@@ -135,6 +135,25 @@ cudaError_t launch_paged_fwd(const PagedTensorMaps &tm, const PagedFwdParams &p,
 constexpr int kPagedTokenRows = 64;
 cudaError_t launch_paged_tokens(const PagedTensorMaps &tm, const PagedFwdParams &p, bool bf16, int sms,
                                 cudaStream_t stream);
+// Launches a kernel that may be set up while the grid before it in the stream
+// still runs; the kernel waits for that one itself (grid_dependency_wait()).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const Args &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Joins the partial results, after either.
 cudaError_t launch_paged_merge(const PagedFwdParams &p, bool bf16, int grid, cudaStream_t stream);
 

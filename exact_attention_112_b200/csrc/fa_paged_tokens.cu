@@ -171,8 +171,6 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    PlanSeqs seqs;
-    if (warp == kPlanWarp) plan_load(p, 0, lane, seqs);    // the tables arrive during the set-up
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
         tmem_relinquish();
@@ -213,6 +211,9 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // Nothing above touches what the stream's earlier grids write or read; this
+    // grid may have been started while the last of them still ran.
+    grid_dependency_wait();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx wctx{p.timeout_ns, p.err, abort_flag};
     auto desc_wait = [&](int u) -> bool {
@@ -226,6 +227,8 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         // ===================== the CTA's share of the work =====================
         MergeMeta mm{0, 0, 0, -1};
         {
+            PlanSeqs seqs;
+            plan_load(p, 0, lane, seqs);
             const Piece pc = plan_piece(p, p.geom, p.min_piece, lane, seqs);
             bool ok = true;
             int u = 0;
@@ -592,10 +595,11 @@ cudaError_t launch_t(const PagedTensorMaps &tm, const PagedFwdParams &p, int gri
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TokenLayout<D, R>::kAlloc);
     if (e != cudaSuccess) return e;
     prof_begin(stream, "fa_paged_tokens_kernel");
-    kern<<<grid, TokenLayout<D, R>::kThreads, TokenLayout<D, R>::kAlloc, stream>>>(tm.q, tm.k, tm.v, p);
+    e = launch_early(kern, dim3(grid), TokenLayout<D, R>::kThreads, TokenLayout<D, R>::kAlloc, stream, tm.q, tm.k, tm.v,
+                     p);
     prof_end(stream);
     note_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     return launch_paged_merge(p, BF16, grid, stream);
 }
 

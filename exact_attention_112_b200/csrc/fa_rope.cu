@@ -31,6 +31,7 @@
 
 #include "fa_internal.h"
 #include "fa_paged_internal.h"
+#include "fa_paged_ptx.cuh"
 
 namespace fa {
 namespace {
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const RopePara
 // page the table does not give, are left alone.
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 3) fa_paged_append_kernel(const AppendParams p, int heads_per_group) {
+    grid_launch_dependents();       // the attention after it may be set up; it waits for this grid
     const int D = p.kv.D;
     const int units = D / 16;
     const int per_block = kRopeThreads / units;

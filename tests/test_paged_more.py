@@ -174,3 +174,50 @@ def test_a_row_of_nan_stays_alone(new):
         for x in ref[:2]:
             x[r] = math.nan
     compare(o, lse, ref)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("new", [[1, 1], [40, 130]])
+def test_waits_for_work_of_two_streams(new, captured):
+    """The call may be set up while the kernel before it still runs, so it has to
+    wait for it and for an event of another stream: the queries come late on one
+    stream, the table on the other."""
+    b = Batch([700, 900], new, 8, 2, 64, 16, "bf16", seed=81).cuda()
+    want, want_lse = b.attend()
+    q, table = b.dq.clone(), b.kv.page_table.clone()
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(b.kv, b.H, b.max_q), dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(b.dq), torch.empty(b.H, b.T, device="cuda")
+    big = torch.randn(4096, 4096, device="cuda")
+    zero = torch.zeros((), device="cuda", dtype=torch.bfloat16)
+    other = torch.cuda.Stream()
+
+    def work():
+        here = torch.cuda.current_stream()
+        b.dq.fill_(7.0)
+        b.kv.page_table.fill_(-1)
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            for _ in range(4):
+                big @ big
+            b.kv.page_table.copy_(table)
+        for _ in range(2):
+            big @ big
+        torch.add(q, zero, out=b.dq)
+        here.wait_stream(other)
+        fa.fa_paged_fwd(b.kv, b.dq, o, lse, b.dcu, b.max_q, ws)
+        o2 = o.clone()              # and what follows it waits for the merge
+        fa.fa_paged_fwd(b.kv, b.dq, o, lse, b.dcu, b.max_q, ws)
+        return o2
+
+    o2 = work()
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o2 = work()
+        for _ in range(3):
+            o.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == fa.FA_OK
+    assert torch.equal(o, want) and torch.equal(lse, want_lse) and torch.equal(o2, want)
