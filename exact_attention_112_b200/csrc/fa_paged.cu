@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(256, 6) fa_paged_merge_kernel(const __grid_con
     float m = neg_inf();
     bool nan = false;                   // of a row of NaN: it stays one
     for (int i = c + lane; i <= mm.last; i += 32) {
-        const float x = p.lse_part[index(i)];
+        const float x = __ldcg(p.lse_part + index(i));
         nan |= x != x;
         m = fmaxf(m, x);
     }
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(256, 6) fa_paged_merge_kernel(const __grid_con
         for (int i0 = c; i0 <= mm.last; i0 += 32) {
             // lane k has the weight of part i0 + k
             const int cnt = min(32, mm.last + 1 - i0);
-            const float wl = lane < cnt ? ex2_approx(p.lse_part[index(i0 + lane)] - m) : 0.f;     // -inf: 0
+            const float wl = lane < cnt ? ex2_approx(__ldcg(p.lse_part + index(i0 + lane)) - m) : 0.f;     // -inf: 0
             // the parts' rows, U loads in flight (more cost the occupancy that many
             // rows of two parts need)
             auto add = [&](auto n, int k) {
@@ -721,10 +721,10 @@ __global__ void __launch_bounds__(256, 6) fa_paged_merge_kernel(const __grid_con
                     w[q] = __shfl_sync(0xffffffffu, wl, (k + q) & 31);
                     const float *src = p.o_part + index(i0 + min(k + q, cnt - 1)) * D + lane * kPer;
                     if constexpr (kPer == 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(src);
+                        const float4 f = __ldcg(reinterpret_cast<const float4 *>(src));
                         v[q][0] = f.x; v[q][1] = f.y; v[q][2] = f.z; v[q][3] = f.w;
                     } else {
-                        const float2 f = *reinterpret_cast<const float2 *>(src);
+                        const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
                         v[q][0] = f.x; v[q][1] = f.y;
                     }
                 }

@@ -349,7 +349,7 @@ def rope_attention_backward(q_rot, k_rot, v, o, lse, dO, rope, positions=None, o
 
 def _cu(what, kv, cu):
     import torch
-    if cu is None or cu.dim() != 1 or cu.dtype != torch.int32 or not cu.is_contiguous():
+    if cu is None or cu.dtype is not torch.int32 or cu.dim() != 1 or not cu.is_contiguous():
         _bad(what, "cu_seqlens_q must be a contiguous int32 vector [num_seqs + 1]")
     if cu.shape[0] != kv.num_seqs + 1:
         _bad(what, f"cu_seqlens_q must have num_seqs + 1 = {kv.num_seqs + 1} entries, got {cu.shape[0]}")
@@ -427,7 +427,7 @@ def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=Tr
     shape = (H, T, kv.D)
     qp, qs = _rows(what, "q", q, shape, kv.dtype, kv.device, D)
     op, os_ = _rows(what, "o", o, shape, kv.dtype, kv.device, D)
-    if lse is None or lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if lse is None or lse.shape != (H, T) or lse.dtype is not torch.float32 or not lse.is_contiguous():
         _bad(what, f"lse must be a contiguous torch.float32 tensor of shape {(H, T)}")
     if lse.device != kv.device:
         _bad(what, f"lse must be on {kv.device}, got {lse.device}")

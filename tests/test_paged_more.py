@@ -221,3 +221,25 @@ def test_waits_for_work_of_two_streams(new, captured):
     torch.cuda.synchronize()
     assert fa.fa_device_status() == fa.FA_OK
     assert torch.equal(o, want) and torch.equal(lse, want_lse) and torch.equal(o2, want)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 2], [12, 3, 20], [60, 1, 140]])
+@pytest.mark.parametrize("pad,off", [(8, 0), (16, 8), (0, 8), (24, 16)])
+def test_strides_of_queries_and_outputs(new, pad, off):
+    """Rows of q and o with padding between them and a base that is 16-byte
+    aligned only: whatever lies between the rows stays as it was."""
+    D = 64
+    b = Batch([200, 90, 310], new, 6, 2, D, 16, "bf16", seed=82).cuda()
+    want, want_lse = b.attend()
+    H, T = b.H, b.T
+    strides = (T * (D + pad) + 8 * (pad > 0), D + pad, 1)
+    q = _strided(b.q, strides, off)
+    buf = torch.full((off + H * strides[0] + 64,), math.nan, dtype=b.dt, device="cuda")
+    o = torch.as_strided(buf, (H, T, D), strides, off)
+    lse = torch.empty(H, T, device="cuda")
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(b.kv, H, b.max_q), dtype=torch.uint8, device="cuda")
+    fa.fa_paged_fwd(b.kv, q, o, lse, b.dcu, b.max_q, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    o.fill_(math.nan)
+    assert torch.isnan(buf).all()
