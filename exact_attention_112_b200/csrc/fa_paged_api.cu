@@ -134,15 +134,15 @@ fa::SchedGeom sched_geom(int G, int max_q) {
     g.unit_tokens = std::max(1, std::min(2 * (128 / G), max_q));
     // Costs, measured: single tokens take 1.5 us a key tile (the memory's rate) and
     // 2 us a unit; in the kernel of row tiles a key tile takes 1.44 us with one,
-    // 2.03 us with two of them, a unit 3 us.
+    // 1.9 us with two of them, a unit 3.2 us.
     if (max_q * G <= fa::kPagedTokenRows) {
         g.tile_tokens = g.unit_tokens;      // one unit per sequence and kv head
         g.unit_cost = 3;
         g.one_cost = g.two_cost = 2;
     } else {
-        g.unit_cost = 10;
-        g.one_cost = 5;
-        g.two_cost = 7;
+        g.unit_cost = 20;
+        g.one_cost = 9;
+        g.two_cost = 12;
     }
     return g;
 }
@@ -306,7 +306,7 @@ int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_stride
     const bool tokens = p.part_rows <= fa::kPagedTokenRows;
     // a key tile at least; two for the kernel of row tiles, which works on two at
     // a time (half a piece holds the first entry of some key tile)
-    p.min_piece = tokens ? 2 : 14;
+    p.min_piece = tokens ? 2 : 24;
     const PagedWorkspace w = paged_workspace(p.geom, G, D);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.o_part = reinterpret_cast<float *>(ws);
