@@ -25,10 +25,11 @@
 // PV(q), S(q + 2) for job after job, across units.
 //
 // Bound by the chain softmax -> P V -> next S of a slot and the hand-overs to
-// the MMA warp: 2020 cycles a job for 1024 of tensor work.  2 x 2048 tokens over
-// 12001..16384 keys (940 GFLOP, H = 32, Hkv = 8, D = 128): 805 us alone, 1168
-// TFLOP/s, 954 us in a long run under the power cap.  A segment of one row tile
-// takes 1.44 us a key tile, at the memory's rate when all CTAs have such.
+// the MMA warp: some 1800 cycles a job for 1024 of tensor work.  2 x 2048 tokens
+// over 12001..16384 keys (940 GFLOP, H = 32, Hkv = 8, D = 128): 731..745 us alone
+// (1260..1285 TFLOP/s), 895..929 in a long run under the power cap.  A segment of
+// one row tile takes 1.44 us a key tile, at the memory's rate when all CTAs have
+// such.
 //
 // Warps: 0-3 and 4-7 softmax of slot 0 and 1 (a thread per row), 8 TMA (its
 // lanes look up a box's page each), 9 MMA, 10 walks the CTA's share of the work
@@ -60,7 +61,6 @@ constexpr uint32_t kRegsSoftmax = 192;
 constexpr uint32_t kRegsOther = 120;
 constexpr int kDescs = 8;           // segment descriptors in the ring
 constexpr float kTau = 8.0f;        // lazy-rescale threshold (log2 units)
-constexpr int kEmuEvery = 4;        // one pair of exponentials in kEmuEvery on the FMA pipe
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D>
@@ -516,11 +516,10 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     m_ref = m_new;
                 }
                 const float m_use = (m_ref == neg_inf()) ? 0.f : m_ref;
-                // p = 2^(x - m) in two halves of 64 keys, each handed to the MMA
-                // warp on its own barrier; one pair in kEmuEvery on the FMA pipe, where
-                // exp2_fma2_quartic gives 2^-126 for a masked score: nothing next to
-                // l >= 1, and a row that has seen no key yet is cleared when it sees
-                // one (alpha = 0) or at the end
+                // p = 2^(x - m) in two halves of 64 keys, each handed to the MMA warp on
+                // its own barrier.  All on the MUFU: a quarter of the pairs on the FMA
+                // pipe, as the other forward has it, costs more in instructions than it
+                // saves here (731 -> 736 us in a burst, 895 -> 925 in a long run).
                 float2 lsum = make_float2(0.f, 0.f), lsum2 = make_float2(0.f, 0.f);
                 const float2 neg_m2 = make_float2(-m_use, -m_use);
                 const float2 qk2 = make_float2(qk, qk);
@@ -530,11 +529,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     for (int c2 = 0; c2 < 32; ++c2) {
                         const int c = 64 * h + 2 * c2;
                         const float2 a = __ffma2_rn(make_float2(x[c], x[c + 1]), qk2, neg_m2);
-                        float2 pp;
-                        if (c2 % kEmuEvery == kEmuEvery - 1)
-                            pp = exp2_fma2_quartic(a);
-                        else
-                            pp = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+                        const float2 pp = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                         if (c2 & 1)
                             lsum2 = __fadd2_rn(lsum2, pp);
                         else
@@ -569,7 +564,6 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
 
             // ---- the rows' results: O = o / l, LSE = (m_ref + log2 l) ln 2
-            if (m_ref == neg_inf() && l == l) l = 0.f;      // no key was seen (a row of NaN stays NaN)
             const int r_tok = row / p.G, r_head = row - r_tok * p.G;
             const int tok = (s.two ? first * p.geom.tile_tokens : 0) + r_tok;
             const bool valid = r_tok < p.geom.tile_tokens && tok < s.ntok;

@@ -45,22 +45,4 @@ __device__ __forceinline__ void tmem_ld32dp_x8_wait(uint32_t taddr, uint32_t (&r
                  : "r"(taddr) : "memory");
 }
 
-// exp2_fma2 with one degree more, for sums that are results themselves (the log
-// of a row's sum is one): 2.9e-6 at most and 3.4e-7 on average over [-1/2, 1/2],
-// where the cubic's average of 4.4e-5 shows in a float32 log-sum-exp.
-__device__ __forceinline__ float2 exp2_fma2_quartic(float2 x) {
-    constexpr float kShift = 12582912.f;   // 1.5 * 2^23
-    constexpr float c1 = 6.931241751e-01f, c2 = 2.402409911e-01f, c3 = 5.590642616e-02f, c4 = 9.582853876e-03f;
-    x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
-    const float2 j = __fadd2_rn(x, make_float2(kShift, kShift));
-    const float2 n = __fadd2_rn(j, make_float2(-kShift, -kShift));
-    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
-    float2 q = __ffma2_rn(make_float2(c4, c4), f, make_float2(c3, c3));
-    q = __ffma2_rn(q, f, make_float2(c2, c2));
-    q = __ffma2_rn(q, f, make_float2(c1, c1));
-    q = __ffma2_rn(q, f, make_float2(1.f, 1.f));
-    return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(j.x) << 23)),
-                       __int_as_float(__float_as_int(q.y) + (__float_as_int(j.y) << 23)));
-}
-
 }  // namespace fa
