@@ -293,12 +293,14 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         };
         Cursor cs, cp;
         int q_n = 0;            // row tiles taken so far
+        const bool lead = elect_one();      // the lane that issues, commits included
+        __syncwarp();
         // S of a job, into the S columns of the slot
         auto issue_s = [&](int slot, int bf, int st, bool k_done, bool q_done) {
             const uint64_t dq = smem_desc_sw128(sbase + L::kQ + bf * L::kTileBytes, 16, 1024);
             const uint64_t dk = KT::k_desc(sbase + L::kK + st * L::kTileBytes);
             const uint32_t d = tmem + L::kColS + slot * 128;
-            if (elect_one()) {
+            if (lead) {
 #pragma unroll 2
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * L::kChunkBytes + (kk & 3) * 32) >> 4;
@@ -340,7 +342,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (int h = 0; h < 2; ++h) {
                 if (!mbar_wait_warp(bar(L::kPHalf + 2 * slot + h), ph, wctx)) return false;
                 tc_fence_after();
-                if (elect_one()) {
+                if (lead) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_f16_ts(d, pa + (4 * h + kk) * 8, dv + KT::v_step(4 * h + kk), idesc_pv, acc || h + kk > 0);
@@ -374,7 +376,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         // waits for K and V stand where it waits for P anyway, and the products of S
         // are rolled by two (2 x 2048 tokens over 16384 keys: 807 us with one general
         // loop and a second variant of the softmax, 739 so; rolled by four 749,
-        // unrolled 748, P V rolled too 770).
+        // unrolled 748, P V rolled too 770; P handed over whole 761 for 737).
         while (ok && cp.jobs > 0) {
             if (cp.two) {
                 const int nt = cp.jobs >> 1, sa = cp.g & 1, sb = sa ^ 1;
@@ -422,7 +424,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
         if (any) {
             // every issued MMA must finish before tensor memory is released
-            if (elect_one()) umma_commit(bar(L::kDrain));
+            if (lead) umma_commit(bar(L::kDrain));
             __syncwarp();
             volatile int zero = 0;
             const WaitCtx drain{wctx.timeout_ns, wctx.err, &zero};
