@@ -130,10 +130,7 @@ def _ptr(t):
 def _stream_ptr(stream):
     if stream is None:
         import torch
-        # the current stream's handle without the Stream object around it (a
-        # third of a small call's time on the host); initialises CUDA if need be
-        torch.cuda.init()
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)

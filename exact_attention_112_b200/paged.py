@@ -19,16 +19,18 @@ import ctypes
 import math
 import struct
 
-from . import FA_ERR_UNSUPPORTED, FA_OK, FaError, _bad, _check, _dtype_code, _stream_ptr, lib
+from . import FA_ERR_UNSUPPORTED, FA_OK, FaError, _bad, _check, _dtype_code, lib
 
 __all__ = ["Rope", "PagedKV", "rope_inv_freq", "fa_rope", "fa_rope_bwd", "rope_forward", "rope_backward",
            "fa_paged_append", "fa_paged_fwd", "fa_paged_fwd_workspace_bytes", "paged_attention", "paged_step",
            "rope_attention_forward", "rope_attention_backward"]
 
 _LL3 = ctypes.c_longlong * 3
-# host arrays of strides, as the bytes that the C side reads during the call
+# host arrays of strides, as the bytes that the C side reads during the call (of
+# four strides the first three)
 _strides2 = struct.Struct("2q").pack
 _strides3 = struct.Struct("3q").pack
+_strides4 = struct.Struct("4q").pack
 
 
 class _RopeSpec(ctypes.Structure):
@@ -180,9 +182,20 @@ class PagedKV:
 
 
 def _on_current(what, device):
+    """Refuse tensors of another device than the current one; returns its index."""
     import torch
-    if device.index != torch._C._cuda_getDevice():
-        _bad(what, f"every tensor must be on the current device cuda:{torch.cuda.current_device()}, got {device}")
+    index = torch._C._cuda_getDevice()
+    if device.index != index:
+        _bad(what, f"every tensor must be on the current device cuda:{index}, got {device}")
+    return index
+
+
+def _stream_of(stream, device_index):
+    """Handle of ``stream``: a torch stream, a raw handle or None (the current one)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _rows(what, name, t, shape, dtype, device, low=0):
@@ -198,8 +211,9 @@ def _rows(what, name, t, shape, dtype, device, low=0):
     if t.device != device:
         _bad(what, f"{name} must be on {device}, got {t.device}")
     st, ptr = t.stride(), t.data_ptr()
-    # the two innermost first: heads and rows, all that a packed tensor has
-    if st[-1] != 1 or (st[-2] | st[-3]) & 7 or st[-2] < low or st[-3] < low or len(st) > 3 or ptr & 15:
+    # rows, heads and batches at once (a packed tensor has no batches); what one of
+    # them is wrong about is found below, where extents of 1 are let through
+    if st[-1] != 1 or (st[-2] | st[-3] | st[0]) & 7 or st[-2] < low or st[-3] < low or st[0] < low or ptr & 15:
         if st[-1] != 1:
             _bad(what, f"{name} rows must be contiguous")
         for n, s in zip(shape, st[:-1]):
@@ -262,7 +276,7 @@ def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream, fresh=
         raise FaError(FA_ERR_UNSUPPORTED, f"{what}: D must be a multiple of 8 from 16 to 512, got {D}")
     if not q.is_cuda:
         _bad(what, f"every tensor must be on a CUDA device, got {q.device}")
-    _on_current(what, q.device)
+    current = _on_current(what, q.device)
     offset = int(offset)
     if rope.device != q.device:
         _bad(what, f"rope must be on {q.device}, got {rope.device}")
@@ -283,10 +297,16 @@ def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream, fresh=
         _bad(what, "k_out without k")
     pp, pstride = _positions(what, positions, B, N, device)
     f = lib().fa_rope if what == "fa_rope" else lib().fa_rope_bwd
-    # [B, H, N, D] has three strides beside the values', packed rows [H, total, D] two
-    three = (lambda st: st and _strides3(*st[:3])) if len(shape) == 4 else (lambda st: st and _strides3(0, *st[:2]))
-    st = f(qp, three(qs), qop, three(qos), shape[-3], kp, three(ks), kop, three(kos), Hk, B, N, D, rope._ref, pp,
-           pstride, offset, code, _stream_ptr(stream))
+    if len(shape) == 4:     # three strides beside the values', packed rows [H, total, D] have two
+        qs, qos = _strides4(*qs), _strides4(*qos)
+        if Hk:
+            ks, kos = _strides4(*ks), _strides4(*kos)
+    else:
+        qs, qos = _strides3(0, qs[0], qs[1]), _strides3(0, qos[0], qos[1])
+        if Hk:
+            ks, kos = _strides3(0, ks[0], ks[1]), _strides3(0, kos[0], kos[1])
+    st = f(qp, qs, qop, qos, shape[-3], kp, ks, kop, kos, Hk, B, N, D, rope._ref, pp, pstride, offset, code,
+           _stream_of(stream, current))
     if st != FA_OK:
         _check(st, what)
 
@@ -361,7 +381,7 @@ def _cu(what, kv, cu):
 def _need_kv(what, kv):
     if not isinstance(kv, PagedKV):
         _bad(what, "kv must be a PagedKV")
-    _on_current(what, kv.device)
+    return _on_current(what, kv.device)
 
 
 def fa_paged_append(kv, k, v, cu_seqlens_q, rope=None, positions=None, q=None, q_out=None, stream=None):
@@ -369,7 +389,7 @@ def fa_paged_append(kv, k, v, cu_seqlens_q, rope=None, positions=None, q=None, q
     total_q, D] of a ragged batch in the cache, and, with q [Hq, total_q, D],
     write the rotated queries to q_out (see include/fa.h)."""
     what = "fa_paged_append"
-    _need_kv(what, kv)
+    current = _need_kv(what, kv)
     if k is None or k.dim() != 3:
         _bad(what, "k must be [num_kv_heads, total_q, D]")
     T, D = k.shape[1], kv.D
@@ -401,7 +421,7 @@ def fa_paged_append(kv, k, v, cu_seqlens_q, rope=None, positions=None, q=None, q
     elif q_out is not None:
         _bad(what, "q_out without q")
     st = lib().fa_paged_append(kv._ref, kp, _strides2(ks[0], ks[1]), vp, _strides2(vs[0], vs[1]), cup, T, ref, pp, qp, qs, qop,
-                               qos, H, _stream_ptr(stream))
+                               qos, H, _stream_of(stream, current))
     if st != FA_OK:
         _check(st, what)
 
@@ -418,7 +438,7 @@ def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=Tr
     its own."""
     import torch
     what = "fa_paged_fwd"
-    _need_kv(what, kv)
+    current = _need_kv(what, kv)
     if q is None or q.dim() != 3:
         _bad(what, "q must be [Hq, total_q, D]")
     H, T, D = q.shape
@@ -439,7 +459,7 @@ def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=Tr
     st = lib().fa_paged_fwd(kv._ref, qp, _strides2(qs[0], qs[1]), op, _strides2(os_[0], os_[1]), lse.data_ptr(), cup, T,
                             int(max_seqlen_q), H, int(bool(causal)),
                             1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+                            workspace.numel() * workspace.element_size(), _stream_of(stream, current))
     if st != FA_OK:
         _check(st, what)
 

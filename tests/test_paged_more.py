@@ -161,8 +161,7 @@ def test_two_graphs_share_a_workspace():
 @pytest.mark.parametrize("new", [[4, 3], [40, 130]])
 def test_a_row_of_nan_stays_alone(new):
     """A query of NaN and one of infinities: NaN comes out, and the other rows are
-    as exact as ever (not the same bits: rows that share a warp choose together on
-    which unit an exponential is computed)."""
+    as exact as ever."""
     b = Batch([300, 400], new, 8, 2, 64, 16, "bf16", seed=76)
     ref = b.ref()
     rows = [(1, 2), (3, new[0] + 1)]
