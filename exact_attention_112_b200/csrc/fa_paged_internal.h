@@ -66,19 +66,23 @@ struct AppendParams {
 
 cudaError_t launch_paged_append(const AppendParams &p, bool bf16, int sms, cudaStream_t stream);
 
-// Sequence b of the batch: its first new row in the packed tensors, new rows
-// and keys, every table entry clamped so that no access can leave the tensors.
+// Sequence b of the batch: its first new row in the packed tensors, the new rows
+// to be computed and keys, every table entry clamped so that no access can leave
+// the tensors.  Row i of them is key i + past of the sequence (the row after the
+// last new one being key len_k), however few of the rows max_q leaves.
 struct PagedSeq {
-    int q0, new_q, len_k;
+    int q0, new_q, len_k, past;
 };
 
 __host__ __device__ inline PagedSeq paged_seq(int b, const int *cu, const int *seq_lens, int total_q, int max_q,
                                               long long capacity) {
     PagedSeq s;
     s.q0 = min(max(cu[b], 0), total_q);
-    s.new_q = min(max(cu[b + 1] - s.q0, 0), min(max_q, total_q - s.q0));
+    const int end = max(cu[b + 1], s.q0);
+    s.new_q = min(end - s.q0, min(max_q, total_q - s.q0));
     const long long len = seq_lens[b];
-    s.len_k = static_cast<int>(len < 0 ? 0 : (len < capacity ? len : capacity));
+    s.len_k = static_cast<int>(len < 0 ? 0 : (len < capacity ? len : capacity));    // at most 2^30
+    s.past = s.len_k - (end - s.q0);
     return s;
 }
 

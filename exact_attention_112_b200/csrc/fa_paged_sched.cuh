@@ -31,7 +31,7 @@ __device__ __forceinline__ int unit_tiles(const PagedSeq &s, int tok0, const Sch
     int vis = s.len_k;
     if (causal) {
         const int last = min(tok0 + g.unit_tokens, s.new_q) - 1;
-        vis = min(vis, last + 1 + s.len_k - s.new_q);
+        vis = min(vis, last + 1 + s.past);
     }
     return vis <= 0 ? 0 : (vis + kPagedTile - 1) / kPagedTile;
 }
@@ -56,6 +56,7 @@ __device__ __forceinline__ long long head_cost(const PagedSeq &s, const SchedGeo
         w.q0 = 0;
         w.new_q = __shfl_sync(0xffffffffu, s.new_q, l);
         w.len_k = __shfl_sync(0xffffffffu, s.len_k, l);
+        w.past = __shfl_sync(0xffffffffu, s.past, l);
         long long sum = 0;
         for (int t = lane * g.unit_tokens; t < w.new_q; t += 32 * g.unit_tokens) sum += unit_cost(w, t, g, causal);
 #pragma unroll
@@ -130,7 +131,7 @@ __device__ __forceinline__ void plan_load(const PagedFwdParams &p, int b0, int l
 #pragma unroll
     for (int i = 0; i < kPlanRounds; ++i) {
         const int b = b0 + 32 * i + lane;
-        q.s[i] = b < p.kv.num_seqs ? load_seq(p, b) : PagedSeq{0, 0, 0};
+        q.s[i] = b < p.kv.num_seqs ? load_seq(p, b) : PagedSeq{0, 0, 0, 0};
     }
 }
 
@@ -188,6 +189,7 @@ __device__ __forceinline__ Piece plan_piece(const PagedFwdParams &p, const Sched
             pc.s.q0 = __shfl_sync(0xffffffffu, q.s[i].q0, l);
             pc.s.new_q = __shfl_sync(0xffffffffu, q.s[i].new_q, l);
             pc.s.len_k = __shfl_sync(0xffffffffu, q.s[i].len_k, l);
+            pc.s.past = __shfl_sync(0xffffffffu, q.s[i].past, l);
             pc.per_head = __shfl_sync(0xffffffffu, head[i], l);
             return pc;
         }
@@ -305,7 +307,7 @@ __device__ __forceinline__ Seg make_seg(const SegWalk &w, const SchedGeom &g) {
     s.h = w.h;
     s.b = w.b;
     s.len_k = w.s.len_k;
-    s.lim0 = w.tok0 + w.s.len_k - w.s.new_q;
+    s.lim0 = w.tok0 + w.s.past;
     s.t0 = w.t0;
     s.nt = w.t1 - w.t0;
     s.two = w.two;

@@ -367,10 +367,13 @@ int fa_paged_append(const fa_paged_kv *kv, const void *k, const long long *k_str
  *              multiple of num_kv_heads, at most 128 times it: head h reads kv
  *              head h / (Hq / num_kv_heads).
  *   lse        [Hq, total_q] float32.
- *   max_seqlen_q  upper bound of the sequences' new rows (a longer one is cut at
- *              the bound).
+ *   max_seqlen_q  upper bound of the sequences' new rows.  Of a sequence with
+ *              more, the first max_seqlen_q are computed, as in a call with the
+ *              full bound, and the others are not written.
  *   causal     1: bottom-right aligned within each sequence, row i of n new
- *              ones sees the keys j <= i + seq_lens[b] - n.  0: all of them.
+ *              ones (n = cu_seqlens_q[b+1] - cu_seqlens_q[b], whatever the
+ *              bound) sees the keys j <= i + seq_lens[b] - n, its own, where
+ *              fa_paged_append() puts it, being the last.  0: all of them.
  *   workspace  fa_paged_fwd_workspace_bytes() bytes, 16-byte aligned, owned by
  *              the caller; contents on entry irrelevant, and calls that may
  *              overlap need one each.

@@ -1,0 +1,52 @@
+"""Rotary positions and the paged cache at the edges of what their calls allow:
+bounds smaller than a sequence, lengths past the table, table entries outside
+the cache, scores near the end of float32, addresses and whole numbers at the
+borders of their ranges, calls that are refused."""
+import math
+
+import pytest
+import torch
+
+import exact_attention_112_b200 as fa
+from exact_attention_112_b200 import paged
+from paged_ref import Batch, compare, rope_ref, rope_tol
+
+gpu = pytest.mark.gpu
+
+
+# ------------------------------------------------- a bound below a sequence's rows
+@gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,new,H,Hkv,D,max_q", [
+    ([320, 70], [5, 2], 4, 4, 64, 3),                   # few rows
+    ([1000, 17, 300], [40, 9, 1], 8, 1, 128, 8),
+    ([3, 10], [9, 10], 2, 1, 64, 4),                    # more rows than keys: the first rows see none
+    ([320, 70], [300, 10], 4, 4, 64, 200),              # row tiles
+    ([2000, 500], [1500, 400], 8, 2, 128, 129),
+    ([50, 700], [300, 650], 4, 2, 64, 270),
+    ([2600], [2600], 4, 1, 64, 2400),                   # more units than a warp has lanes
+])
+def test_rows_below_the_bound_are_those_of_the_whole_call(lens, new, H, Hkv, D, max_q, causal):
+    """Row i of n new ones sees the keys up to i + length - n, whatever the bound
+    leaves of the n: the rows that are computed are the uncut call's."""
+    b = Batch(lens, new, H, Hkv, D, 16, "bf16", seed=max_q).cuda()
+    ref = b.ref(causal)
+    for s, n in enumerate(new):
+        for x in ref[:2]:
+            x[:, int(b.cu[s]) + min(n, max_q):int(b.cu[s + 1])] = math.nan      # not computed, left as they were
+    compare(*b.attend(causal, max_q=max_q), ref)
+
+
+@gpu
+@pytest.mark.parametrize("rows", [4, 90])
+def test_a_table_that_ends_past_the_rows(rows):
+    """Row t of the packed tensors is key length - cu_seqlens_q[b + 1] + t, also
+    where the table's last entry lies past them."""
+    whole = Batch([400, 300], [2, 2 * rows], 8, 2, 64, 16, "bf16", seed=5).cuda()
+    ref = whole.ref()
+    T = 2 + rows
+    o, lse = torch.empty_like(whole.dq[:, :T]), torch.empty(8, T, device="cuda")
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(whole.kv, 8, 2 * rows), dtype=torch.uint8, device="cuda")
+    fa.fa_paged_fwd(whole.kv, whole.dq[:, :T], o, lse, whole.dcu, 2 * rows, ws)
+    torch.cuda.synchronize()
+    compare(o, lse, [x[:, :T] for x in ref])
