@@ -220,11 +220,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa_paged_append_kernel(const 
     if (b >= p.kv.num_seqs) return;
     const int first = __ldg(p.cu + b), end = __ldg(p.cu + b + 1);
     if (t < first) return;
-    // position in the sequence: its last token sits at length - 1
-    const long long at = static_cast<long long>(__ldg(p.kv.seq_lens + b)) - end + t;
+    // position in the sequence: its last token sits at length - 1, the length clamped
+    // as the attention's
+    const int capacity = p.kv.max_pages * p.kv.page_size;       // at most 2^30
+    const long long at = static_cast<long long>(min(max(__ldg(p.kv.seq_lens + b), 0), capacity)) - end + t;
     long long page = -1;
     int row = 0;
-    if (at >= 0 && at < static_cast<long long>(p.kv.max_pages) * p.kv.page_size) {
+    if (at >= 0 && at < capacity) {
         const int pi = static_cast<int>(at) / p.kv.page_size;
         row = static_cast<int>(at) - pi * p.kv.page_size;
         page = __ldg(p.kv.table + b * p.kv.table_stride + pi);

@@ -323,9 +323,11 @@ int fa_rope_bwd(const void *dq_out, const long long *dq_out_strides, void *dq,
  *                     most 2^30.
  *   D, dtype          64 or 128; FA_F16 or FA_BF16.
  * The tables are read on the device only.  Lengths are clamped to
- * [0, max_pages * page_size]; a page index outside [0, num_pages) is never
- * followed: what would be stored there is dropped and its keys and values
- * read as zeros.  Entries past a sequence's last page are not read.
+ * [0, max_pages * page_size], by fa_paged_append() and fa_paged_fwd() alike
+ * (seq_lens[b] below stands for the clamped one); a page index outside
+ * [0, num_pages) is never followed: what would be stored there is dropped and
+ * its keys and values read as zeros.  Entries past a sequence's last page are
+ * not read.
  */
 typedef struct fa_paged_kv {
     void *k_cache, *v_cache;

@@ -50,3 +50,24 @@ def test_a_table_that_ends_past_the_rows(rows):
     fa.fa_paged_fwd(whole.kv, whole.dq[:, :T], o, lse, whole.dcu, 2 * rows, ws)
     torch.cuda.synchronize()
     compare(o, lse, [x[:, :T] for x in ref])
+
+
+# ----------------------------------------------------- lengths past the page table
+@gpu
+@pytest.mark.parametrize("new", [[1, 2, 2, 1], [5, 64, 2, 3], [40, 64, 2, 30]])
+def test_append_and_attention_clamp_lengths_alike(new):
+    """Lengths above max_pages * page_size or below 0: the new rows are stored and
+    rotated at the clamped length's last positions, and see the keys up to them."""
+    from test_paged import _expected_cache, _same
+    b = Batch([64, 64, 0, 50], new, 8, 2, 64, 16, "bf16", seed=sum(new)).cuda()
+    b.kv.seq_lens.copy_(torch.tensor([64 + 3, 10 ** 9, -5, 50], dtype=torch.int32))
+    f, _ = fa.rope_inv_freq(64)
+    qo = torch.full_like(b.dq, math.nan)
+    fa.fa_paged_append(b.kv, b.dkn, b.dvn, b.dcu, rope=fa.Rope(f), q=b.dq, q_out=qo)
+    torch.cuda.synchronize()
+    k, v, tol, qr, qt = _expected_cache(b, f.cpu(), False)
+    _same(b.dk, k, tol)
+    _same(b.dv, v, torch.zeros_like(v))
+    _same(qo, qr, qt)
+    b.k, b.v = b.dk.cpu(), b.dv.cpu()
+    compare(*b.attend(), b.ref())
