@@ -224,6 +224,14 @@ def _rows(what, name, t, shape, dtype, device, low=0):
     return ptr, st
 
 
+def _int32(what, name, x):
+    """`x` as an int that a C int holds: ctypes would take it modulo 2^32."""
+    x = int(x)
+    if not -2147483648 <= x <= 2147483647:
+        _bad(what, f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 _AS_IT_IS = contextlib.nullcontext()
 
 
@@ -274,10 +282,10 @@ def _rope_call(what, q, k, q_out, k_out, rope, positions, offset, stream, fresh=
         _bad(what, f"rot_dim {rope.rot_dim} exceeds D {D}")
     if D % 8 or D < 16 or D > 512:
         raise FaError(FA_ERR_UNSUPPORTED, f"{what}: D must be a multiple of 8 from 16 to 512, got {D}")
+    offset = _int32(what, "offset", offset)
     if not q.is_cuda:
         _bad(what, f"every tensor must be on a CUDA device, got {q.device}")
     current = _on_current(what, q.device)
-    offset = int(offset)
     if rope.device != q.device:
         _bad(what, f"rope must be on {q.device}, got {rope.device}")
     dtype, device = q.dtype, q.device
@@ -427,6 +435,10 @@ def fa_paged_append(kv, k, v, cu_seqlens_q, rope=None, positions=None, q=None, q
 
 
 def fa_paged_fwd_workspace_bytes(kv, Hq, max_seqlen_q) -> int:
+    what = "fa_paged_fwd_workspace_bytes"
+    if not isinstance(kv, PagedKV):
+        _bad(what, "kv must be a PagedKV")
+    Hq, max_seqlen_q = _int32(what, "Hq", Hq), _int32(what, "max_seqlen_q", max_seqlen_q)
     return int(lib().fa_paged_fwd_workspace_bytes(kv._ref, Hq, max_seqlen_q))
 
 
@@ -453,11 +465,12 @@ def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=Tr
         _bad(what, f"lse must be on {kv.device}, got {lse.device}")
     if workspace is None or not workspace.is_contiguous() or workspace.device != kv.device:
         _bad(what, f"workspace must be a contiguous tensor on {kv.device}")
+    max_seqlen_q = _int32(what, "max_seqlen_q", max_seqlen_q)
     if max_seqlen_q < 0:
         _bad(what, "max_seqlen_q must be >= 0")
     cup = _cu(what, kv, cu_seqlens_q)
     st = lib().fa_paged_fwd(kv._ref, qp, _strides2(qs[0], qs[1]), op, _strides2(os_[0], os_[1]), lse.data_ptr(), cup, T,
-                            int(max_seqlen_q), H, int(bool(causal)),
+                            max_seqlen_q, H, int(bool(causal)),
                             1.0 / math.sqrt(D) if scale is None else float(scale), workspace.data_ptr(),
                             workspace.numel() * workspace.element_size(), _stream_of(stream, current))
     if st != FA_OK:

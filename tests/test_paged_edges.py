@@ -71,3 +71,44 @@ def test_append_and_attention_clamp_lengths_alike(new):
     _same(qo, qr, qt)
     b.k, b.v = b.dk.cpu(), b.dv.cpu()
     compare(*b.attend(), b.ref())
+
+
+# ------------------------------------------------------ whole numbers past 32 bits
+def _handle(cls, **kw):
+    """A handle without its tensors: refusals that come before they are looked at."""
+    x = object.__new__(cls)
+    x.__dict__.update(kw)
+    return x
+
+
+@pytest.mark.parametrize("offset", [2 ** 31, 2 ** 32, 2 ** 32 + 7, -2 ** 31 - 1, 2 ** 63, -2 ** 40])
+def test_offsets_past_32_bits_are_refused(offset):
+    q = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
+    rope = _handle(fa.Rope, rot_dim=64)
+    calls = [lambda: fa.rope_forward(q, q, rope, offset=offset), lambda: fa.rope_backward(q, None, rope, offset=offset),
+             lambda: fa.fa_rope(q, None, q, None, rope, offset=offset),
+             lambda: fa.fa_rope_bwd(q, q, q, q, rope, offset=offset),
+             lambda: fa.rope_attention_forward(q, q, q, rope, offset=offset)]
+    for call in calls:
+        with pytest.raises(fa.FaError, match="offset"):
+            call()
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32, 2 ** 32 + 4, -2 ** 31 - 1, 2 ** 64 + 1])
+def test_sizes_past_32_bits_are_refused(n):
+    kv = _handle(fa.PagedKV, num_kv_heads=2, num_seqs=1, D=64)
+    for args, name in (((4, n), "max_seqlen_q"), ((n, 1), "Hq")):
+        with pytest.raises(fa.FaError, match=name):
+            fa.fa_paged_fwd_workspace_bytes(kv, *args)
+
+
+@gpu
+def test_a_bound_past_32_bits_is_refused_by_the_calls():
+    b = Batch([40], [3], 4, 2, 64, 16, "bf16", seed=7).cuda()
+    o, lse = torch.empty_like(b.dq), torch.empty(4, 3, device="cuda")
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(b.kv, 4, 3), dtype=torch.uint8, device="cuda")
+    for n in (2 ** 32, 2 ** 32 + 3, -2 ** 32 + 3):
+        with pytest.raises(fa.FaError, match="max_seqlen_q"):
+            fa.fa_paged_fwd(b.kv, b.dq, o, lse, b.dcu, n, ws)
+        with pytest.raises(fa.FaError, match="max_seqlen_q"):
+            fa.paged_attention(b.kv, b.dq, b.dcu, n)
