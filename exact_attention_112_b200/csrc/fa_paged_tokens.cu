@@ -42,7 +42,9 @@ namespace {
 constexpr int kBN = kPagedTile;     // keys per tile
 constexpr int kDescs = 8;           // segment descriptors in the ring
 constexpr float kTau = 8.0f;        // a row's reference maximum moves past this (log2 units)
-constexpr float kNone = -1e30f;     // reference maximum of a row that has seen no key
+// Reference maximum of a row that has seen no key: every finite score lies above
+// it (with -inf the subtraction of a masked score would give NaN).
+constexpr float kNone = -3.402823466e38f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // What the threads share of a row, beside its reference maximum: the factor that

@@ -112,3 +112,51 @@ def test_a_bound_past_32_bits_is_refused_by_the_calls():
             fa.fa_paged_fwd(b.kv, b.dq, o, lse, b.dcu, n, ws)
         with pytest.raises(fa.FaError, match="max_seqlen_q"):
             fa.paged_attention(b.kv, b.dq, b.dcu, n)
+
+
+# --------------------------------------------------------- scores far below nothing
+@gpu
+@pytest.mark.parametrize("lens,new", [([1, 100, 128], [1, 1, 2]), ([70, 100, 128], [60, 1, 100])])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_near_the_end_of_float32(lens, new, D):
+    """Every score of a row is the same -2^116 scale (operands and scale factors
+    are powers of two, so float32 has it exactly): the keys have equal weights.
+    The probabilities are 1 and their sum a whole number below 2^8, so O is off by
+    one rounding, the quotient's and n float32 additions' 2^-24."""
+    b = Batch(lens, new, 4, 2, D, 16, "bf16", seed=D)
+    b.q.zero_()
+    b.q[..., 5] = -2.0 ** 58
+    held = ~torch.isnan(b.k)
+    b.k[held] = 0.0
+    b.k[..., 5][held[..., 5]] = 2.0 ** 58
+    b.cuda()
+    scale = 0.125
+    o, lse = (x.double().cpu() for x in b.attend(scale=scale))
+    for s, n in enumerate(lens):
+        j = torch.arange(n)
+        v = b.v[b.table[s].long()[j // 16], :, j % 16].double().repeat_interleave(2, 1)        # [n, H, D]
+        for t in range(int(b.cu[s]), int(b.cu[s + 1])):
+            seen = n - int(b.cu[s + 1]) + t + 1
+            want, size = v[:seen].mean(0), v[:seen].abs().mean(0)
+            assert ((o[:, t] - want).abs() <= 2.0 ** -8 * want.abs() + (seen + 4) * 2.0 ** -24 * size).all()
+            assert ((lse[:, t] + 2.0 ** 116 * scale).abs() <= 2.0 ** 116 * scale * 2.0 ** -22).all()
+
+
+@gpu
+@pytest.mark.parametrize("new", [1, 90])
+def test_the_highest_of_very_low_scores_takes_all(new):
+    """Over several key tiles and CTAs: one key's score is -2^115 scale, all others
+    are -2^116 scale, so O is its value."""
+    b = Batch([1000], [new], 4, 2, 64, 16, "bf16", seed=9)
+    b.q.zero_()
+    b.q[..., 5] = -2.0 ** 58
+    held = ~torch.isnan(b.k)
+    b.k[held] = 0.0
+    b.k[..., 5][held[..., 5]] = 2.0 ** 58
+    at = 700
+    page = int(b.table[0, at // 16])
+    b.k[page, :, at % 16, 5] = 2.0 ** 57
+    b.cuda()
+    o, _ = b.attend(scale=0.125)
+    want = b.v[page, :, at % 16].repeat_interleave(2, 0)[:, None].expand(-1, new, -1)
+    assert torch.equal(o.cpu(), want)
