@@ -282,7 +282,7 @@ int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_stride
     if (!cu_seqlens_q || !aligned(cu_seqlens_q, 4)) return FA_ERR_INVALID_ARG;
     if (total_q == 0 || max_seqlen_q == 0) return FA_OK;
     if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 16)) return FA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16)) return FA_ERR_INVALID_ARG;
     const long long n[2] = {Hq, total_q};
     long long s[2];
     if ((st = get_strides(q_strides, n, kv->D, kv->D, s)) != FA_OK) return st;

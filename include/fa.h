@@ -368,7 +368,7 @@ int fa_paged_append(const fa_paged_kv *kv, const void *k, const long long *k_str
  *   q, o       [Hq, total_q, D] with *_strides as in fa_paged_append(); Hq is a
  *              multiple of num_kv_heads, at most 128 times it: head h reads kv
  *              head h / (Hq / num_kv_heads).
- *   lse        [Hq, total_q] float32.
+ *   lse        [Hq, total_q] float32, contiguous, 4-byte aligned (q and o 16-byte).
  *   max_seqlen_q  upper bound of the sequences' new rows.  Of a sequence with
  *              more, the first max_seqlen_q are computed, as in a call with the
  *              full bound, and the others are not written.

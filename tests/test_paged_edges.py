@@ -160,3 +160,35 @@ def test_the_highest_of_very_low_scores_takes_all(new):
     o, _ = b.attend(scale=0.125)
     want = b.v[page, :, at % 16].repeat_interleave(2, 0)[:, None].expand(-1, new, -1)
     assert torch.equal(o.cpu(), want)
+
+
+# ------------------------------------------------------------------- where LSE lies
+@pytest.mark.parametrize("low", [4, 8, 12])
+def test_lse_needs_the_alignment_of_a_float(low):
+    """16-byte alignment is for rows of O and Q; LSE is single floats.  Without a
+    workspace the call ends before anything of it is touched."""
+    import ctypes
+    from exact_attention_112_b200 import _build
+    from test_paged_api import P, _kv
+    _build.build()
+    call = lambda lse: fa.lib().fa_paged_fwd(_kv(), P(1), None, P(2), None, ctypes.c_void_p(lse), P(4), 4, 1, 4, 1, 0.1,
+                                             None, 0, None)
+    assert call(48) == fa.FA_ERR_WORKSPACE
+    assert call(48 + low) == fa.FA_ERR_WORKSPACE
+    assert call(48 + 2) == fa.FA_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("new", [[1, 1, 1], [5, 1, 90]])
+def test_lse_in_the_middle_of_a_buffer(new, off):
+    b = Batch([300, 17, 1000], new, 6, 2, 64, 16, "bf16", seed=off).cuda()
+    want, want_lse = b.attend()
+    buf = torch.full((off + b.H * b.T + 5,), 7.0, device="cuda")
+    lse = buf[off:off + b.H * b.T].view(b.H, b.T)
+    o = torch.empty_like(b.dq)
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(b.kv, b.H, b.max_q), dtype=torch.uint8, device="cuda")
+    fa.fa_paged_fwd(b.kv, b.dq, o, lse, b.dcu, b.max_q, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert (buf[:off] == 7.0).all() and (buf[off + b.H * b.T:] == 7.0).all()
