@@ -99,6 +99,9 @@ struct PagedLayout {
     static_assert(sizeof(Seg) % 16 == 0, "descriptors are copied as int4");
 };
 
+// Rows of O in 32-byte stores, whole sectors, where their alignment allows it (a
+// first prompt of 8192 tokens 526 us with 16-byte stores, 501 with these; 1 prompt
+// among 63 single tokens 233 and 228).
 __device__ __forceinline__ void st_global_v8(void *p, const uint32_t *a) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a[0]), "r"(a[1]),
                  "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])

@@ -293,6 +293,7 @@ int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_stride
     const int G = Hq / kv->num_kv_heads, D = kv->D;
     const bool bf16 = kv->dtype == FA_BF16;
     p.o = o;
+    p.o_v8 = aligned(o, 32) && p.o_h % 16 == 0 && p.o_n % 16 == 0;
     p.lse = lse;
     p.cu = cu_seqlens_q;
     p.T = total_q;

@@ -192,3 +192,24 @@ def test_lse_in_the_middle_of_a_buffer(new, off):
     torch.cuda.synchronize()
     assert torch.equal(o, want) and torch.equal(lse, want_lse)
     assert (buf[:off] == 7.0).all() and (buf[off + b.H * b.T:] == 7.0).all()
+
+
+# ------------------------------------------- what the kernels read is what is set
+@pytest.mark.parametrize("struct,source", [("PagedFwdParams", "fa_paged_api.cu"), ("AppendParams", "fa_paged_api.cu"),
+                                           ("RopeParams", "fa_paged_api.cu")])
+def test_every_parameter_of_the_kernels_is_set(struct, source):
+    """A field that a kernel reads and the host never sets leaves one of its paths
+    to nobody."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(fa.__file__), "csrc")
+    with open(os.path.join(csrc, "fa_paged_internal.h")) as f:
+        body = re.search(r"struct %s \{(.*?)\n\};" % struct, f.read(), re.S).group(1)
+    with open(os.path.join(csrc, source)) as f:
+        text = f.read()
+    fields = []
+    for line in re.sub(r"//.*", "", body).split(";"):
+        names = line.replace("*", " ").split(",")
+        fields += [n.split()[-1] for n in names if n.split()]
+    unset = [f for f in fields if not re.search(r"\bp\.%s(\.\w+)? = |&p\.%s\b|\(p\.%s, " % (f, f, f), text)]
+    assert fields and not unset, f"{struct}: nothing sets {unset}"
