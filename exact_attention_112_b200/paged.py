@@ -442,6 +442,18 @@ def fa_paged_fwd_workspace_bytes(kv, Hq, max_seqlen_q) -> int:
     return int(lib().fa_paged_fwd_workspace_bytes(kv._ref, Hq, max_seqlen_q))
 
 
+def _heads(what, kv, H):
+    if H % kv.num_kv_heads or not 1 <= H // kv.num_kv_heads <= 128:
+        _bad(what, f"Hq must be 1 to 128 times the cache's {kv.num_kv_heads} heads, got {H}")
+
+
+def _bound(what, max_seqlen_q):
+    max_seqlen_q = _int32(what, "max_seqlen_q", max_seqlen_q)
+    if max_seqlen_q < 0:
+        _bad(what, f"max_seqlen_q must be >= 0, got {max_seqlen_q}")
+    return max_seqlen_q
+
+
 def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=True, scale=None, stream=None):
     """Attention of the new rows q [Hq, total_q, D] of a ragged batch over the
     paged cache into caller-owned o (same shape) and lse float32 [Hq, total_q],
@@ -454,8 +466,7 @@ def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=Tr
     if q is None or q.dim() != 3:
         _bad(what, "q must be [Hq, total_q, D]")
     H, T, D = q.shape
-    if H % kv.num_kv_heads or not 1 <= H // kv.num_kv_heads <= 128:
-        _bad(what, f"Hq must be 1 to 128 times the cache's {kv.num_kv_heads} heads, got {H}")
+    _heads(what, kv, H)
     shape = (H, T, kv.D)
     qp, qs = _rows(what, "q", q, shape, kv.dtype, kv.device, D)
     op, os_ = _rows(what, "o", o, shape, kv.dtype, kv.device, D)
@@ -465,9 +476,7 @@ def fa_paged_fwd(kv, q, o, lse, cu_seqlens_q, max_seqlen_q, workspace, causal=Tr
         _bad(what, f"lse must be on {kv.device}, got {lse.device}")
     if workspace is None or not workspace.is_contiguous() or workspace.device != kv.device:
         _bad(what, f"workspace must be a contiguous tensor on {kv.device}")
-    max_seqlen_q = _int32(what, "max_seqlen_q", max_seqlen_q)
-    if max_seqlen_q < 0:
-        _bad(what, "max_seqlen_q must be >= 0")
+    max_seqlen_q = _bound(what, max_seqlen_q)
     cup = _cu(what, kv, cu_seqlens_q)
     st = lib().fa_paged_fwd(kv._ref, qp, _strides2(qs[0], qs[1]), op, _strides2(os_[0], os_[1]), lse.data_ptr(), cup, T,
                             max_seqlen_q, H, int(bool(causal)),
@@ -495,8 +504,23 @@ def paged_step(kv, q, k, v, cu_seqlens_q, max_seqlen_q, rope=None, positions=Non
                stream=None):
     """One layer's attention of a serving step: store the new keys and values
     (rotated, and q with them, when there is a rope), then attend over the
-    cache.  Returns (o, lse)."""
+    cache.  Returns (o, lse).  A call that is refused has stored nothing."""
     import torch
+    what = "paged_step"
+    # what the attention would refuse, ahead of the append (which checks the rest)
+    _need_kv(what, kv)
+    if q is None or q.dim() != 3:
+        _bad(what, "q must be [Hq, total_q, D]")
+    H, T = q.shape[:2]
+    _heads(what, kv, H)
+    _rows(what, "q", q, (H, T, kv.D), kv.dtype, kv.device, kv.D if rope is None else 0)
+    if H * T > 2147483647:
+        _bad(what, f"Hq * total_q must fit in 31 bits, got {H} * {T}")
+    _bound(what, max_seqlen_q)
+    if scale is not None and not 0.0 < ctypes.c_float(float(scale)).value < math.inf:
+        _bad(what, f"scale must be finite and > 0 in float32, got {scale}")
+    if rope is None and positions is not None:
+        _bad(what, "positions need a rope")
     q_rot = q
     if rope is not None:
         with _allocating_on(stream):

@@ -213,3 +213,31 @@ def test_every_parameter_of_the_kernels_is_set(struct, source):
         fields += [n.split()[-1] for n in names if n.split()]
     unset = [f for f in fields if not re.search(r"\bp\.%s(\.\w+)? = |&p\.%s\b|\(p\.%s, " % (f, f, f), text)]
     assert fields and not unset, f"{struct}: nothing sets {unset}"
+
+
+# ------------------------------------------------ a step that is refused as a whole
+@gpu
+def test_a_refused_step_leaves_the_cache_as_it_was():
+    """paged_step stores before it attends: what the attention refuses must not
+    have been stored, and nothing that was asked for may go unheard."""
+    b = Batch([40, 33], [3, 2], 4, 2, 64, 16, "bf16", seed=17).cuda()
+    f, _ = fa.rope_inv_freq(64)
+    rope = fa.Rope(f)
+    before = [x.clone().view(torch.int16) for x in (b.dk, b.dv)]
+    pos = torch.arange(b.T, dtype=torch.int32, device="cuda")
+    q3 = b.dq[:3].contiguous()
+    wide = b.dq[:1].expand(4, -1, -1)                   # heads on top of one another
+    same = dict(kv=b.kv, q=b.dq, k=b.dkn, v=b.dvn, cu_seqlens_q=b.dcu, max_seqlen_q=3)
+    for match, kw in [("positions", dict(positions=pos)), ("scale", dict(scale=0.0)), ("scale", dict(scale=math.nan)),
+                      ("scale", dict(rope=rope, scale=math.inf)), ("max_seqlen_q", dict(max_seqlen_q=-1)),
+                      ("max_seqlen_q", dict(rope=rope, max_seqlen_q=2 ** 32)), ("Hq must be", dict(q=q3)),
+                      ("Hq must be", dict(q=q3, rope=rope)), ("q must be", dict(q=None)),
+                      ("must have shape", dict(q=b.dq[:, :4], rope=rope)), ("strides", dict(q=wide)), ("cu_seqlens_q", dict(cu_seqlens_q=b.dcu[:2])),
+                      ("kv must be", dict(kv=None))]:
+        with pytest.raises(fa.FaError, match=match):
+            fa.paged_step(**dict(same, **kw))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x.view(torch.int16), y) for x, y in zip((b.dk, b.dv), before))
+    o, _ = fa.paged_step(**dict(same, q=wide, rope=rope))      # rotated into rows of their own: fine
+    want, _ = fa.paged_step(**dict(same, q=wide.contiguous(), rope=rope))
+    assert torch.equal(o, want)
