@@ -160,8 +160,8 @@ class PagedKV:
             _bad(what, "page_table rows must be contiguous and apart")
         if self.num_seqs > 1 and seq_lens.stride(0) != 1:
             _bad(what, "seq_lens must be contiguous")
-        if self.num_pages < 1 or self.max_pages * self.page_size > 1 << 30:
-            _bad(what, "the cache needs a page, and max_pages * page_size must be at most 2^30")
+        if self.num_pages < 1 or self.num_kv_heads < 1 or self.max_pages * self.page_size > 1 << 30:
+            _bad(what, "the cache needs a page and a head, and max_pages * page_size must be at most 2^30")
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
             if t.stride(3) != 1 or any(n > 1 and (s % 8 or s < self.D) for n, s in zip(t.shape[:3], t.stride()[:3])):
                 _bad(what, f"{name} rows must be contiguous, with strides that are multiples of 8 and at least D")

@@ -241,3 +241,9 @@ def test_a_refused_step_leaves_the_cache_as_it_was():
     o, _ = fa.paged_step(**dict(same, q=wide, rope=rope))      # rotated into rows of their own: fine
     want, _ = fa.paged_step(**dict(same, q=wide.contiguous(), rope=rope))
     assert torch.equal(o, want)
+
+
+def test_a_cache_without_heads_is_refused():
+    k = torch.zeros(3, 0, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(fa.FaError, match="a head"):
+        fa.PagedKV(k, k, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
