@@ -232,8 +232,8 @@ def test_a_refused_step_leaves_the_cache_as_it_was():
                       ("scale", dict(rope=rope, scale=math.inf)), ("max_seqlen_q", dict(max_seqlen_q=-1)),
                       ("max_seqlen_q", dict(rope=rope, max_seqlen_q=2 ** 32)), ("Hq must be", dict(q=q3)),
                       ("Hq must be", dict(q=q3, rope=rope)), ("q must be", dict(q=None)),
-                      ("must have shape", dict(q=b.dq[:, :4], rope=rope)), ("strides", dict(q=wide)), ("cu_seqlens_q", dict(cu_seqlens_q=b.dcu[:2])),
-                      ("kv must be", dict(kv=None))]:
+                      ("must have shape", dict(q=b.dq[:, :4], rope=rope)), ("strides", dict(q=wide)),
+                      ("cu_seqlens_q", dict(cu_seqlens_q=b.dcu[:2])), ("kv must be", dict(kv=None))]:
         with pytest.raises(fa.FaError, match=match):
             fa.paged_step(**dict(same, **kw))
     torch.cuda.synchronize()
@@ -247,3 +247,58 @@ def test_a_cache_without_heads_is_refused():
     k = torch.zeros(3, 0, 16, 64, dtype=torch.bfloat16)
     with pytest.raises(fa.FaError, match="a head"):
         fa.PagedKV(k, k, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+
+
+# -------------------------------------------------------- entries outside the cache
+@gpu
+@pytest.mark.parametrize("rope", [False, True])
+@pytest.mark.parametrize("tokens", [False, True])
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 90, 5]])
+def test_rows_for_pages_outside_the_cache_are_dropped(new, tokens, rope):
+    """New rows whose table entry is -1 or num_pages.  The caches lie between
+    canary pages of the same allocation, where such a row would be stored, and
+    every other slot is compared bit by bit."""
+    S, Hkv, D, pad = 16, 2, 64, 4
+    b = Batch([70, 100, 33], new, 4, Hkv, D, S, "bf16", seed=33)
+    P = b.k.shape[0]
+    bad = [(0, 69 // S, -1), (1, 99 // S, P), (1, 10 // S, -1)]        # the first two hold their sequence's last row
+    for s, i, entry in bad:
+        b.table[s, i] = entry
+    g = torch.Generator().manual_seed(1)
+    big = [torch.randint(-2 ** 15, 2 ** 15, (P + 2 * pad, Hkv, S, D), generator=g, dtype=torch.int16) for _ in range(2)]
+    for x, c in zip(big, (b.k, b.v)):
+        x[pad:pad + P] = c.view(torch.int16)
+    if tokens:
+        dev = [x.transpose(1, 2).contiguous().cuda().transpose(1, 2) for x in big]
+    else:
+        dev = [x.cuda() for x in big]
+    b.cuda()
+    kv = fa.PagedKV(*(x[pad:pad + P].view(torch.bfloat16) for x in dev), b.table.cuda(), b.seq_lens.cuda())
+    f, _ = fa.rope_inv_freq(64)
+    if rope:
+        qo = torch.full_like(b.dq, math.nan)
+        fa.fa_paged_append(kv, b.dkn, b.dvn, b.dcu, rope=fa.Rope(f), q=b.dq, q_out=qo)
+    else:
+        fa.fa_paged_append(kv, b.dkn, b.dvn, b.dcu)
+    torch.cuda.synchronize()
+    got = [x.cpu() for x in dev]
+    dropped = 0
+    for s, n in enumerate(b.lens):
+        for t in range(int(b.cu[s]), int(b.cu[s + 1])):
+            at = n - int(b.cu[s + 1]) + t
+            page = int(b.table[s, at // S])
+            if not 0 <= page < P:
+                dropped += 1
+                continue
+            if rope:        # within the bound; then as it came, so that the whole buffer can be compared
+                x = b.k_new[:, t].double()[:, None]
+                y = rope_ref(x, torch.tensor([at]), f.cpu())
+                z = got[0][pad + page, :, at % S].view(torch.bfloat16).double()[:, None]
+                assert ((z - y).abs() <= rope_tol(x, y, f.cpu(), torch.bfloat16)).all()
+                big[0][pad + page, :, at % S] = got[0][pad + page, :, at % S]
+            else:
+                big[0][pad + page, :, at % S] = b.k_new[:, t].view(torch.int16)
+            big[1][pad + page, :, at % S] = b.v_new[:, t].view(torch.int16)
+    assert dropped >= 2 and all(torch.equal(x, y) for x, y in zip(got, big))
+    if rope:                # the queries of dropped rows are rotated all the same
+        assert not torch.isnan(qo).any()
