@@ -26,10 +26,11 @@
 //
 // Bound by the chain softmax -> P V -> next S of a slot and the hand-overs to
 // the MMA warp: some 1800 cycles a job for 1024 of tensor work.  2 x 2048 tokens
-// over 12001..16384 keys (940 GFLOP, H = 32, Hkv = 8, D = 128): 731..745 us alone
-// (1260..1285 TFLOP/s), 895..929 in a long run under the power cap.  A segment of
-// one row tile takes 1.44 us a key tile, at the memory's rate when all CTAs have
-// such.
+// over 12001..16384 keys (940 GFLOP, H = 32, Hkv = 8, D = 128): 719..736 us alone
+// (1280..1310 TFLOP/s), 902..926 in a long run under the power cap.  The chain is
+// no shorter at D = 64, where the products are half: the same tokens 660..670 us
+// (470 GFLOP, 288 us at the tensor cores' rate).  A segment of one row tile takes
+// 1.34..1.57 us a key tile, at the memory's rate when all CTAs have such.
 //
 // Warps: 0-3 and 4-7 softmax of slot 0 and 1 (a thread per row), 8 TMA (its
 // lanes look up a box's page each), 9 MMA, 10 walks the CTA's share of the work
@@ -522,9 +523,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 const float m_use = (m_ref == neg_inf()) ? 0.f : m_ref;
                 // p = 2^(x - m) in two halves of 64 keys, each handed to the MMA warp on
-                // its own barrier.  All on the MUFU: a quarter of the pairs on the FMA
-                // pipe, as the other forward has it, costs more in instructions than it
-                // saves here (731 -> 736 us in a burst, 895 -> 925 in a long run).
+                // its own barrier, rounded to the operands' type: the tensor cores take A
+                // and B of one type, and P in two pieces (high and low) would double the
+                // product.  The sum l takes p unrounded.  All on the MUFU: a quarter of
+                // the pairs on the FMA pipe, as the other forward has it, gains in a burst
+                // (2 x 2048 tokens over 12001..16384 keys: D = 128 719 -> 707 us, D = 64
+                // 663 -> 614) and loses in long runs (D = 128 904 -> 912, with single
+                // tokens 353 -> 360), and a quartic's error is in LSE.
                 float2 lsum = make_float2(0.f, 0.f), lsum2 = make_float2(0.f, 0.f);
                 const float2 neg_m2 = make_float2(-m_use, -m_use);
                 const float2 qk2 = make_float2(qk, qk);

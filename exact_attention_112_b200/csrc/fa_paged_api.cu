@@ -132,9 +132,11 @@ fa::SchedGeom sched_geom(int G, int max_q) {
     fa::SchedGeom g;
     g.tile_tokens = std::max(1, std::min(128 / G, max_q));
     g.unit_tokens = std::max(1, std::min(2 * (128 / G), max_q));
-    // Costs, measured: single tokens take 1.5 us a key tile (the memory's rate) and
-    // 2 us a unit; in the kernel of row tiles a key tile takes 1.44 us with one,
-    // 1.9 us with two of them, a unit 3.2 us.
+    // Costs, measured at D = 128: single tokens take 1.5 us a key tile (the memory's
+    // rate) and 2 us a unit; in the kernel of row tiles a key tile takes 1.34..1.57 us
+    // with one, 1.79..2.02 us with two of them, a unit 3.2 us.  D = 64 goes by the
+    // same ones, though its key tiles with one row tile are cheaper (0.90..0.96 us,
+    // with two 1.66..1.79): units of both kinds in a batch are shared out less evenly.
     if (max_q * G <= fa::kPagedTokenRows) {
         g.tile_tokens = g.unit_tokens;      // one unit per sequence and kv head
         g.unit_cost = 3;

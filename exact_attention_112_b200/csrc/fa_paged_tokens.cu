@@ -18,8 +18,8 @@
 // spread over the threads until the unit's end.
 //
 // Measured (D = 128, G = 4): 64 tokens over 512..8192 keys in pages of 16, 1143
-// MB, 185 us, 6.16 TB/s; one token over 65536 keys, 8 heads, 55.9 us (41 at the
-// copy rate); one over 1000 keys 7 us and 2.5 of merging.  With row tiles of 128
+// MB, 181..184 us, 6.2..6.3 TB/s; one token over 65536 keys, 8 heads, 54.9 us (41
+// at the copy rate); one over 1000 keys 7 us and 2.5 of merging.  With row tiles of 128
 // for those rows (fa_paged.cu) the first took 255 us: the softmax of one tile
 // held its V for longer than the ring covers.
 //
@@ -520,7 +520,9 @@ fa_paged_tokens_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     }
                     subtract();
                 }
-                // P = 2^a, rounded to the operands' type; masked keys give 0
+                // P = 2^a, rounded to the operands' type (the tensor cores take A and B of
+                // one type, and V comes as it is); the sums take it unrounded.  Masked
+                // keys give 0.
                 uint8_t *const pt = p_key + (t & 1) * L::kPBytes;
 #pragma unroll
                 for (int r = 0; r < C; r += 2) {

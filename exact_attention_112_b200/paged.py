@@ -354,7 +354,8 @@ def rope_backward(dq_out, dk_out, rope, positions=None, offset=0, stream=None):
 def rope_attention_forward(q, k, v, rope, positions=None, offset=0, causal=False, scale=None, key_bias=None,
                            stream=None):
     """attention_forward of the rotated q and k; returns (o, lse, q_rot, k_rot),
-    the last two for rope_attention_backward."""
+    the last two for rope_attention_backward.  Like attention_forward it takes as
+    many heads of k and v as of q; grouped ones are rotated by rope_forward."""
     from . import attention_forward
     with _allocating_on(stream):
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()

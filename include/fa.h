@@ -385,6 +385,12 @@ int fa_paged_append(const fa_paged_kv *kv, const void *k, const long long *k_str
  * have to be finite (a masked 0 times NaN is NaN, as in the other forwards).  A
  * query row of NaN gives NaN in its own row only.  The result does not
  * depend on timing: the same call gives the same bits.
+ * Scores, sums, partial results and LSE are float32.  The probabilities are
+ * rounded to the type of q for the product with V, as in the other 16-bit
+ * forwards, while their sum adds them unrounded: O is off by that rounding,
+ * averaged over the keys, and by its own.  Rows whose scores reach 2^26 in
+ * magnitude leave the range in which float32 tells their keys apart, and may
+ * lose probabilities.
  */
 size_t fa_paged_fwd_workspace_bytes(const fa_paged_kv *kv, int Hq, int max_seqlen_q);
 int fa_paged_fwd(const fa_paged_kv *kv, const void *q, const long long *q_strides, void *o,
